@@ -90,6 +90,7 @@ struct Layout {
   size_t partials = 0;
   size_t coef = 0, urows = 0, ucount = 0;
   size_t coef_hl = 0;  // M > 1: the coefficients' bf16 head and tail for the tensor-core GEMV
+  size_t mx4 = 0;      // the 4-bit sparse linear's coefficients (d_in a multiple of its block)
   size_t total = 0;
   bool list_gemv = false;  // M = 1: the row-streaming GEMV over a list of up to d_in rows fits
 };
@@ -178,6 +179,7 @@ int make_layout_uncached(int M, int d_in, int d_out, int K, Layout* L) {
     L->ucount = take(4);
     L->coef_hl = take((size_t)2 * M * d_in * 2);  // the tensor-core path's coefficient rows
   }
+  if (d_in % LAROSA_MX4_BLOCK == 0) L->mx4 = take(larosa::mx4_rows_buffer_bytes(M, d_in));
   L->total = off;
   return LAROSA_OK;
 }
@@ -991,6 +993,96 @@ int larosa_dense_linear(const void* x, const void* Wt, int M, int d_in, int d_ou
   if (!rowdot_aligned(Wt, x, d_in)) return LAROSA_ERR_ALIGN;
   return run_rowdot(x, Wt, y, M, d_in, d_out, dtype, reinterpret_cast<cudaStream_t>(stream),
                     "dense kernel");
+}
+
+static int check_mx4_matrix(int rows, int cols, int axis) {
+  if (axis != 0 && axis != 1) return LAROSA_ERR_INVALID_ARG;
+  if (rows < 1 || cols < 1) return LAROSA_ERR_SHAPE;
+  if (cols % LAROSA_MX4_BLOCK != 0 || (axis == 0 && rows % LAROSA_MX4_BLOCK != 0)) return LAROSA_ERR_ALIGN;
+  return LAROSA_OK;
+}
+
+int larosa_mx4_quantize(const void* src, int rows, int cols, int axis, int dtype, void* codes, void* scales,
+                        int* dev_status, larosa_stream_t stream) {
+  if (!valid_dtype(dtype)) return LAROSA_ERR_UNSUPPORTED_DTYPE;
+  if (src == nullptr || codes == nullptr || scales == nullptr) return LAROSA_ERR_INVALID_ARG;
+  const int st = check_mx4_matrix(rows, cols, axis);
+  if (st != LAROSA_OK) return st;
+  if (!aligned16(src) || !aligned16(codes) || !aligned16(scales)) return LAROSA_ERR_ALIGN;
+  const cudaError_t e = larosa::launch_mx4_quantize(src, rows, cols, axis, elem_of(dtype), codes, scales,
+                                                    dev_status, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LAROSA_OK : cuda_fail(e, "quantise kernel");
+}
+
+int larosa_mx4_dequantize(const void* codes, const void* scales, int rows, int cols, int axis, int dtype,
+                          void* dst, larosa_stream_t stream) {
+  if (!valid_dtype(dtype)) return LAROSA_ERR_UNSUPPORTED_DTYPE;
+  if (dst == nullptr || codes == nullptr || scales == nullptr) return LAROSA_ERR_INVALID_ARG;
+  const int st = check_mx4_matrix(rows, cols, axis);
+  if (st != LAROSA_OK) return st;
+  if (!aligned16(dst) || !aligned16(codes) || !aligned16(scales)) return LAROSA_ERR_ALIGN;
+  const cudaError_t e = larosa::launch_mx4_dequantize(codes, scales, rows, cols, axis, elem_of(dtype), dst,
+                                                      reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LAROSA_OK : cuda_fail(e, "dequantise kernel");
+}
+
+// A 4-bit weight [d_in x d_out] with its blocks down the rows.
+static int check_mx4_rows(int d_in, int d_out, const void* codes, const void* scales) {
+  if (d_in % LAROSA_MX4_BLOCK != 0 || d_out % LAROSA_MX4_BLOCK != 0 || !aligned16(codes) || !aligned16(scales))
+    return LAROSA_ERR_ALIGN;
+  return LAROSA_OK;
+}
+
+int larosa_mx4_sparse_linear(const int32_t* idx, const float* val, int M, int K, const void* W_codes,
+                             const void* W_scales, int d_in, int d_out, float* y, void* ws, size_t ws_bytes,
+                             int* dev_status, larosa_stream_t stream) {
+  if (W_codes == nullptr || W_scales == nullptr || y == nullptr || (K > 0 && (idx == nullptr || val == nullptr)))
+    return LAROSA_ERR_INVALID_ARG;
+  int st = check_sizes(M, d_in, d_out, K);
+  if (st != LAROSA_OK) return st;
+  st = check_mx4_rows(d_in, d_out, W_codes, W_scales);
+  if (st != LAROSA_OK) return st;
+  if (!aligned16(y)) return LAROSA_ERR_ALIGN;
+  Layout L;
+  st = make_layout(M, d_in, d_out, K, &L);
+  if (st != LAROSA_OK) return st;
+  st = workspace_ok(ws, ws_bytes, L);
+  if (st != LAROSA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = debug_check_lists(idx, val, M, K, d_in, false, dev_status, s);
+  if (st != LAROSA_OK) return st;
+  void* buf = at(ws, L.mx4);
+  cudaError_t e = cudaSuccess;
+  const bool list = M == 1 && K > 0;  // one token's list is read by the product's CTAs themselves
+  if (!list) e = larosa::launch_mx4_coef(idx, val, M, K, d_in, buf, dev_status, s);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit coefficient kernel");
+  e = larosa::launch_mx4_rows(list ? idx : nullptr, val, K, buf, M, W_codes, W_scales, d_in, d_out, y, dev_status, s);
+  return e == cudaSuccess ? LAROSA_OK : cuda_fail(e, "4-bit sparse linear kernel");
+}
+
+int larosa_mx4_topk_linear(const float* x_rot, const void* W_codes, const void* W_scales, int M, int d_in,
+                           int d_out, int K, float* y, void* ws, size_t ws_bytes, int* dev_status,
+                           larosa_stream_t stream) {
+  if (x_rot == nullptr || W_codes == nullptr || W_scales == nullptr || y == nullptr) return LAROSA_ERR_INVALID_ARG;
+  int st = check_sizes(M, d_in, d_out, K);
+  if (st != LAROSA_OK) return st;
+  st = check_mx4_rows(d_in, d_out, W_codes, W_scales);
+  if (st != LAROSA_OK) return st;
+  if (!aligned16(x_rot) || !aligned16(y)) return LAROSA_ERR_ALIGN;
+  Layout L;
+  st = make_layout(M, d_in, d_out, K, &L);
+  if (st != LAROSA_OK) return st;
+  st = workspace_ok(ws, ws_bytes, L);
+  if (st != LAROSA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int32_t* idx = reinterpret_cast<int32_t*>(at(ws, L.idx));
+  float* val = reinterpret_cast<float*>(at(ws, L.val));
+  void* buf = at(ws, L.mx4);
+  cudaError_t e = larosa::launch_topk(x_rot, M, d_in, K, idx, val, dev_status, s, nullptr, buf);
+  if (e != cudaSuccess) return cuda_fail(e, "topk kernel");
+  e = larosa::launch_mx4_rows(nullptr, nullptr, K, buf, M, W_codes, W_scales, d_in, d_out, y, dev_status, s);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit sparse linear kernel");
+  return check_workspace_lists(M, d_in, d_out, K, ws, dev_status, stream);
 }
 
 int larosa_check(const int* dev_status, larosa_stream_t stream, int* flags_out) {

@@ -7,6 +7,10 @@
 
 namespace larosa {
 
+namespace mx4 {
+struct Operand;  // mx4_mma.cuh
+}
+
 // Geometry of one launch of the row-streaming GEMV (see rowstream.cu).
 struct GemvPlan {
   int col_tile = 0;        // Wc: output columns per CTA
@@ -58,8 +62,11 @@ cudaError_t launch_gemv(const GemvArgs& a, const GemvPlan& plan, cudaStream_t st
 // Top-K: one 1024-thread CTA per token.  With hl != nullptr (d a multiple of
 // 8) it also writes the tokens' dense coefficient rows as bf16 head and tail
 // for the tensor-core sparse linear: hl[m][0, d) heads, hl[M + m][0, d) tails.
+// With mx4_buf != nullptr (d a multiple of 32) it writes them for the 4-bit
+// sparse linear, as launch_mx4_coef does.
 cudaError_t launch_topk(const float* x_rot, int M, int d, int K, int32_t* idx, float* val,
-                        int* dev_status, cudaStream_t stream, __nv_bfloat16* hl = nullptr);
+                        int* dev_status, cudaStream_t stream, __nv_bfloat16* hl = nullptr,
+                        void* mx4_buf = nullptr);
 
 // The same dense head/tail coefficient rows from given kept lists (idx/val
 // [M x K], indices distinct within a row): one CTA per token.
@@ -261,5 +268,27 @@ cudaError_t launch_lowrank(Elem w_elem, const LowrankArgs& a, const StreamPlan& 
 // W_rot = Qt . W with Qt = Q^T given row-major.
 cudaError_t launch_prepare(const void* Q, const void* W, void* W_rot, int d_in, int d_out,
                            Elem elem, cudaStream_t stream);
+
+// Microscaled 4-bit format (mx4.cu): values to codes and scales and back,
+// blocks of 32 along a row (axis 1) or down a column (axis 0).
+cudaError_t launch_mx4_quantize(const void* src, int rows, int cols, int axis, Elem elem, void* codes,
+                                void* scales, int* dev_status, cudaStream_t stream);
+cudaError_t launch_mx4_dequantize(const void* codes, const void* scales, int rows, int cols, int axis,
+                                  Elem elem, void* dst, cudaStream_t stream);
+
+// Sparse linear with a 4-bit weight [d_in x d_out], blocks down the rows
+// (mx4_rows.cu); d_in and d_out multiples of 32.  The coefficients come as one
+// token's kept list (idx not null, M = 1) or in `buf`
+// (mx4_rows_buffer_bytes): dense fp32 rows [M x d_in], or from 5 tokens on
+// (mx4_rows_take_operand) the tensor-core operand mx4_rows_operand describes.
+// launch_mx4_coef fills `buf` from kept lists; so does launch_topk.
+bool mx4_rows_take_operand(int M);
+size_t mx4_rows_buffer_bytes(int M, int d_in);
+mx4::Operand mx4_rows_operand(void* buf, int M, int d_in);
+cudaError_t launch_mx4_coef(const int32_t* idx, const float* val, int M, int K, int d_in, void* buf,
+                            int* dev_status, cudaStream_t stream);
+cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, const void* buf, int M, const void* codes,
+                            const void* scales, int d_in, int d_out, float* y, int* dev_status,
+                            cudaStream_t stream);
 
 }  // namespace larosa

@@ -15,6 +15,7 @@
 #include "coef.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "mx4_mma.cuh"
 #include "select.cuh"
 
 namespace larosa {
@@ -41,10 +42,12 @@ __device__ __forceinline__ void write_head_tail(const uint32_t* bits, int d, Kep
 
 // With hl != nullptr the kernel also writes each token's dense coefficient
 // rows for the tensor-core product: hl[m][0, d) the heads, hl[M + m][0, d)
-// the tails (d a multiple of 8).
+// the tails (d a multiple of 8); with coef != nullptr the fp32 row (x where
+// kept, else 0), and with op.piece != nullptr the token's operand of the
+// 4-bit sparse linear (d a multiple of 32).
 __global__ void __launch_bounds__(kTopkThreads, 1)
     topk_kernel(const float* __restrict__ x_rot, int d, int K, int32_t* __restrict__ idx,
-                float* __restrict__ val, int* dev_status, __nv_bfloat16* hl) {
+                float* __restrict__ val, int* dev_status, __nv_bfloat16* hl, float* coef, mx4::Operand op) {
   // raw fp32 bits of the row, padded with zero keys to a multiple of 4: a
   // zero key at an index >= d loses every tie, so padding is never kept
   extern __shared__ __align__(16) uint32_t bits[];
@@ -122,6 +125,15 @@ __global__ void __launch_bounds__(kTopkThreads, 1)
     write_head_tail(bits, d, [&](uint32_t key, int i) { return is_kept(key, i, e); }, hl + (size_t)m * d,
                     hl + (M + m) * d);
   }
+  auto kept_value = [&](int i) {
+    const uint32_t u = bits[i];
+    return is_kept(u & kKeyMask, i, e) ? __uint_as_float(u) : 0.f;
+  };
+  if (coef != nullptr)
+    for (int i = tid; i < d; i += kTopkThreads) coef[(size_t)m * d + i] = kept_value(i);
+  if (op.piece != nullptr)
+    for (int b = tid >> 5; b < d / mx4::kBlock; b += kTopkThreads / 32)
+      op.put(b, m, kept_value(b * 32 + (tid & 31)), tid & 31);
 }
 
 // The tokens' dense coefficient rows for the tensor-core sparse linear, from
@@ -265,8 +277,8 @@ cudaError_t launch_coef_rows(const int32_t* idx, const float* val, int M, int K,
 }
 
 cudaError_t launch_topk(const float* x_rot, int M, int d, int K, int32_t* idx, float* val,
-                        int* dev_status, cudaStream_t stream, __nv_bfloat16* hl) {
-  if (hl != nullptr && d % 8 != 0) return cudaErrorInvalidValue;
+                        int* dev_status, cudaStream_t stream, __nv_bfloat16* hl, void* mx4_buf) {
+  if ((hl != nullptr && d % 8 != 0) || (mx4_buf != nullptr && d % mx4::kBlock != 0)) return cudaErrorInvalidValue;
   const size_t smem = (size_t)((d + 3) & ~3) * sizeof(uint32_t);
   static int configured[64] = {0};  // per device: dynamic shared memory limit raised
   int dev = 0;
@@ -288,7 +300,10 @@ cudaError_t launch_topk(const float* x_rot, int M, int d, int K, int32_t* idx, f
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, topk_kernel, x_rot, d, K, idx, val, dev_status, hl);
+  const bool operand = mx4_buf != nullptr && mx4_rows_take_operand(M);
+  return cudaLaunchKernelEx(&cfg, topk_kernel, x_rot, d, K, idx, val, dev_status, hl,
+                            operand ? nullptr : static_cast<float*>(mx4_buf),
+                            operand ? mx4_rows_operand(mx4_buf, M, d) : mx4::Operand{});
 }
 
 }  // namespace larosa

@@ -53,6 +53,10 @@ _SIGNATURES = {
     "larosa_lowrank_workspace_bytes": ([_i, _i, _i, _i, _i], _sz),
     "larosa_sparse_linear_noalloc": ([_vp, _vp, _i, _i, _vp, _i, _i, _vp, _i, _vp, _vp], _i),
     "larosa_sparse_linear_noalloc_bytes": ([_i, _i, _i, _i, _i], _sz),
+    "larosa_mx4_quantize": ([_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp], _i),
+    "larosa_mx4_dequantize": ([_vp, _vp, _i, _i, _i, _i, _vp, _vp], _i),
+    "larosa_mx4_sparse_linear": ([_vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
+    "larosa_mx4_topk_linear": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
     "larosa_workspace_sync_offset": ([_i, _i, _i, _i, _c.POINTER(_sz)], _i),
     "larosa_set_wait_limit_ns": ([_c.c_uint64, _c.POINTER(_c.c_uint64)], _i),
     "larosa_set_debug": ([_i, _c.POINTER(_i)], _i),
@@ -81,6 +85,7 @@ LAROSA_DEV_LIST = 0x8
 LAROSA_MAX_SPLIT_K = 8
 LAROSA_MAX_M = 16
 LAROSA_MAX_D = 32768
+LAROSA_MX4_BLOCK = 32
 LAROSA_NOALLOC_SCRATCH_BYTES = 2 << 20
 
 
@@ -540,6 +545,158 @@ def larosa_dense_linear(x: torch.Tensor, Wt: torch.Tensor, y: torch.Tensor | Non
     _need(y, "y", torch.float32)
     _check(_lib.larosa_dense_linear(_ptr(x2), _ptr(Wt), M, d_in, d_out, _ptr(y), _dtype_code(x),
                                     _stream(x.device)), "larosa_dense_linear")
+    return y
+
+
+# The calls below are short next to what Python spends around them (a one-token
+# product takes 5 to 10 us on the device), so they pass plain integers to
+# ctypes, ask for the raw stream and enter a device context only where the
+# tensors' device is not the current one.
+
+def _need_fast(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device) -> None:
+    """_need, and on the device of the call's other tensors."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.device == device
+            and t.is_contiguous()):
+        _need(t, name, dtype)
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+
+
+def _out(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, device) -> torch.Tensor:
+    """An output: allocated when not given, else checked (type, device, size)."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need_fast(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _call(fn, where: str, device: torch.device, *args) -> None:
+    """fn(*args, stream) on the tensors' device, on its current stream."""
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status != LAROSA_OK:
+        raise LarosaError(status, where)
+
+
+def _status_word(dev_status: torch.Tensor | None, device: torch.device) -> int:
+    if dev_status is None:
+        st = _status_cache.get(device.index)
+        return (default_status(device) if st is None else st).data_ptr()
+    _need_fast(dev_status, "dev_status", torch.int32, device)
+    return dev_status.data_ptr()
+
+
+def _ws_pair(ws, device: torch.device, *sizes) -> tuple[int, int]:
+    """(address, bytes) of a workspace for these sizes; ws: a Workspace, a
+    tensor, or None for the current stream's own."""
+    if ws is None:
+        ws = default_workspace(device)
+    buf = ws.get(*sizes) if isinstance(ws, Workspace) else ws
+    if buf.device != device:
+        raise ValueError(f"the workspace is on {buf.device}, the other tensors are on {device}")
+    return buf.data_ptr(), buf.numel() * buf.element_size()
+
+
+def _mx4_shapes(shape: tuple, axis: int) -> tuple[tuple, tuple, int, int]:
+    """(codes shape, scales shape, rows, cols) of a matrix or a stack of them
+    ([..., rows, cols]; the stacked matrices' rows follow one another)."""
+    if axis != 0 and axis != 1:
+        raise ValueError("axis must be 0 or 1")
+    if len(shape) < 2:
+        raise ValueError("expected a matrix or a stack of matrices")
+    r, c = shape[-2], shape[-1]
+    b = LAROSA_MX4_BLOCK
+    if c % b or (axis == 0 and r % b):
+        raise ValueError(f"the blocked axis and the rows must be multiples of {b}")
+    if len(shape) == 2:
+        return (r, c // 2), ((r, c // b) if axis == 1 else (r // b, c)), r, c
+    lead = tuple(shape[:-2])
+    n = 1
+    for k in lead:
+        n *= k
+    return lead + (r, c // 2), lead + ((r, c // b) if axis == 1 else (r // b, c)), n * r, c
+
+
+def larosa_mx4_quantize(src: torch.Tensor, axis: int = 1, codes: torch.Tensor | None = None,
+                        scales: torch.Tensor | None = None, dev_status: torch.Tensor | None = None
+                        ) -> tuple[torch.Tensor, torch.Tensor]:
+    """A matrix (or a stack of matrices, [..., rows, cols]) in microscaled 4-bit
+    form: (codes uint8 [..., rows, cols / 2], scales uint8).  axis 1: blocks of
+    32 along a row, scales [..., rows, cols / 32]; axis 0: down a column, scales
+    [..., rows / 32, cols].  See larosa_mx4_quantize in the header."""
+    _need(src, "src")
+    dev = src.device
+    cs, ss, rows, cols = _mx4_shapes(src.shape, axis)
+    codes = _out(codes, "codes", cs, torch.uint8, dev)
+    scales = _out(scales, "scales", ss, torch.uint8, dev)
+    _call(_lib.larosa_mx4_quantize, "larosa_mx4_quantize", dev, src.data_ptr(), rows, cols, axis,
+          _dtype_code(src), codes.data_ptr(), scales.data_ptr(), _status_word(dev_status, dev))
+    return codes, scales
+
+
+def _mx4_pair(codes: torch.Tensor, scales: torch.Tensor, axis: int, what: str) -> tuple[int, int]:
+    """Checks a (codes, scales) pair; returns its (rows, cols)."""
+    _need(codes, what + "codes", torch.uint8)
+    _need_fast(scales, what + "scales", torch.uint8, codes.device)
+    shape = codes.shape
+    if len(shape) < 2:
+        raise ValueError(f"{what}codes must be a matrix or a stack of matrices")
+    _, ss, rows, cols = _mx4_shapes((*shape[:-1], 2 * shape[-1]), axis)
+    if scales.shape != ss:
+        raise ValueError(f"{what}scales must have shape {ss}, got {tuple(scales.shape)}")
+    return rows, cols
+
+
+def larosa_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, axis: int = 1,
+                          dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that codes and scales (larosa_mx4_quantize) stand for."""
+    rows, cols = _mx4_pair(codes, scales, axis, "")
+    out = _out(out, "out", (*codes.shape[:-1], cols), dtype if out is None else out.dtype, codes.device)
+    _call(_lib.larosa_mx4_dequantize, "larosa_mx4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(),
+          rows, cols, axis, _dtype_code(out), out.data_ptr())
+    return out
+
+
+def larosa_mx4_sparse_linear(idx: torch.Tensor, val: torch.Tensor, W_codes: torch.Tensor, W_scales: torch.Tensor,
+                             y: torch.Tensor | None = None, ws=None, dev_status: torch.Tensor | None = None
+                             ) -> torch.Tensor:
+    """y = sum_k val[:, k] * W[idx[:, k]], fp32 [M, d_out], with a 4-bit weight
+    (W_codes, W_scales of larosa_mx4_quantize(W, axis=0))."""
+    d_in, d_out = _mx4_pair(W_codes, W_scales, 0, "W_")
+    dev = W_codes.device
+    _need_fast(idx, "idx", torch.int32, dev)
+    _need_fast(val, "val", torch.float32, dev)
+    idx, val = _as2d(idx), _as2d(val)
+    if idx.shape != val.shape or W_codes.dim() != 2:
+        raise ValueError("idx and val must have one shape [M, K], W_codes [d_in, d_out / 2]")
+    M, K = idx.shape
+    y = _out(y, "y", (M, d_out), torch.float32, dev)
+    p, n = _ws_pair(ws, dev, M, d_in, d_out, K)
+    _call(_lib.larosa_mx4_sparse_linear, "larosa_mx4_sparse_linear", dev, idx.data_ptr(), val.data_ptr(), M, K,
+          W_codes.data_ptr(), W_scales.data_ptr(), d_in, d_out, y.data_ptr(), p, n, _status_word(dev_status, dev))
+    return y
+
+
+def larosa_mx4_topk_linear(x_rot: torch.Tensor, W_codes: torch.Tensor, W_scales: torch.Tensor, K: int,
+                           y: torch.Tensor | None = None, ws=None, dev_status: torch.Tensor | None = None
+                           ) -> torch.Tensor:
+    """larosa_topk_linear with a 4-bit weight (W_codes, W_scales of
+    larosa_mx4_quantize(W, axis=0)); the kept list stays in the workspace."""
+    d_in, d_out = _mx4_pair(W_codes, W_scales, 0, "W_")
+    dev = W_codes.device
+    _need_fast(x_rot, "x_rot", torch.float32, dev)
+    x_rot = _as2d(x_rot)
+    M = x_rot.shape[0]
+    if x_rot.shape[1] != d_in or W_codes.dim() != 2:
+        raise ValueError("x_rot must be [M, d_in], W_codes [d_in, d_out / 2]")
+    y = _out(y, "y", (M, d_out), torch.float32, dev)
+    p, n = _ws_pair(ws, dev, M, d_in, d_out, K)
+    _call(_lib.larosa_mx4_topk_linear, "larosa_mx4_topk_linear", dev, x_rot.data_ptr(), W_codes.data_ptr(),
+          W_scales.data_ptr(), M, d_in, d_out, K, y.data_ptr(), p, n, _status_word(dev_status, dev))
     return y
 
 

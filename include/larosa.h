@@ -78,6 +78,7 @@ typedef struct CUstream_st *larosa_stream_t;
 #define LAROSA_VERSION 100 /* 1.0.0 */
 #define LAROSA_MAX_M 16
 #define LAROSA_MAX_D 32768
+#define LAROSA_MX4_BLOCK 32 /* values that share a scale in the 4-bit format */
 
 /* Return codes. */
 typedef enum {
@@ -396,6 +397,71 @@ int larosa_sparse_linear_noalloc(const int32_t *idx, const float *val, int M,
  */
 size_t larosa_sparse_linear_noalloc_bytes(int M, int d_in, int d_out, int K,
                                           int dtype);
+
+/*
+ * Microscaled 4-bit storage (MX4; the Open Compute Project's MXFP4).  A
+ * matrix is held as
+ *   codes   [rows x cols / 2] bytes: two 4-bit floats (e2m1: 0, 0.5, 1, 1.5,
+ *           2, 3, 4, 6 and their negatives; sign in the high bit) per byte,
+ *           the even column in the low half;
+ *   scales  one byte b per block of LAROSA_MX4_BLOCK = 32 values, standing
+ *           for 2^(b - 127), b = 255 for NaN.
+ * The blocks run along the reduction of the product the matrix is for:
+ *   axis 1  along a row (activations; weights in torch.nn.Linear layout):
+ *           scales [rows x cols / 32];
+ *   axis 0  down a column (row-major [d_in x d_out] weights, whose rows are
+ *           gathered): scales [rows / 32 x cols].
+ * cols is a multiple of 32, and so is rows for axis 0; codes, scales and the
+ * values 16-byte aligned.  Stacked matrices ([E x d_in x d_out]) are one
+ * matrix of E d_in rows.
+ *
+ * larosa_mx4_quantize: b = floor(log2(max |v|)) - 2 + 127 over the block,
+ * not below 0; an all-zero block takes 0.  Each value divided by the scale is
+ * rounded to the nearest 4-bit float, ties to even, and values of 5 to 8
+ * scales saturate at 6.  A block with a NaN or Inf gets b = 255 and codes of
+ * zero (it reads back as NaN) and sets LAROSA_DEV_NONFINITE.
+ * src: [rows x cols] of `dtype`.
+ */
+int larosa_mx4_quantize(const void *src, int rows, int cols, int axis,
+                        int dtype, void *codes, void *scales, int *dev_status,
+                        larosa_stream_t stream);
+
+/* The values codes and scales stand for, dst: [rows x cols] of `dtype`.
+ * Exact in both types (up to overflow beyond their largest value). */
+int larosa_mx4_dequantize(const void *codes, const void *scales, int rows,
+                          int cols, int axis, int dtype, void *dst,
+                          larosa_stream_t stream);
+
+/*
+ * larosa_sparse_linear with a 4-bit weight:
+ *   y[m][j] = sum_k val[m][k] * W[idx[m][k]][j],
+ * W [d_in x d_out] held as W_codes and W_scales with axis 0 (for example
+ * larosa_prepare_weights' W_rot quantised with axis 0).  Only blocks and rows
+ * that some token keeps are read.  idx/val as for larosa_sparse_linear; fp32
+ * accumulation, with the coefficients exact to 2^-24 of themselves (2^-50 of
+ * the largest of their token within the 32 rows of a block); finite
+ * coefficients below 2^100 in magnitude.  An index outside [0, d_in) sets
+ * LAROSA_DEV_INDEX and contributes nothing.  d_in and d_out multiples of 32;
+ * W_codes, W_scales and y 16-byte aligned.  y: [M x d_out] fp32; results
+ * repeat bit for bit.  ws: at least larosa_workspace_bytes(M, d_in, d_out, K)
+ * bytes (it holds the tokens' coefficients between the call's two kernels).
+ */
+int larosa_mx4_sparse_linear(const int32_t *idx, const float *val, int M,
+                             int K, const void *W_codes, const void *W_scales,
+                             int d_in, int d_out, float *y, void *ws,
+                             size_t ws_bytes, int *dev_status,
+                             larosa_stream_t stream);
+
+/*
+ * larosa_topk_linear with a 4-bit weight: the Top-K of an already rotated
+ * vector (larosa_topk's rule) and the product above.  x_rot: [M x d_in] fp32,
+ * 16-byte aligned; ws: at least larosa_workspace_bytes(M, d_in, d_out, K)
+ * bytes; the kept lists lie at the offsets larosa_workspace_layout gives.
+ */
+int larosa_mx4_topk_linear(const float *x_rot, const void *W_codes,
+                           const void *W_scales, int M, int d_in, int d_out,
+                           int K, float *y, void *ws, size_t ws_bytes,
+                           int *dev_status, larosa_stream_t stream);
 
 /*
  * Workspace bytes sufficient for every entry point above called with these

@@ -33,6 +33,10 @@ Functions and the passages they follow (page title, section):
                         compensation A_r = U_r S_r^1/2, B_r = S_r^1/2 V_r^T and
                         the hybrid output y ~ y_s + y_r).
 
+* ``mx4_quantize``, ``mx4_values``  the microscaled 4-bit storage of weights and
+                        activations (the Open Compute Project's MXFP4): not on
+                        the pages.
+
 Readings where the pages are silent:
 
 * orientation: activations are row vectors, x_rot = x . Q, so the weight is
@@ -57,4 +61,6 @@ from .larosa_ref import (  # noqa: F401
     threshold_select,
     lowrank_factors,
     sparse_lowrank_linear,
+    mx4_quantize,
+    mx4_values,
 )

@@ -212,3 +212,53 @@ def sparse_lowrank_linear(x, W, A_r, B_r, idx) -> np.ndarray:
     y_s = kept[idx] @ W[idx]
     y_r = (dropped @ np.asarray(A_r, dtype=np.float64)) @ np.asarray(B_r, dtype=np.float64)
     return y_s + y_r
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _mx4_blocks(a: np.ndarray, axis: int) -> np.ndarray:
+    """[blocks, 32] view of a matrix's blocks (a copy for axis 0)."""
+    return (a if axis == 1 else a.T).reshape(-1, 32)
+
+
+def mx4_quantize(x, axis: int) -> tuple[np.ndarray, np.ndarray]:
+    """Microscaled 4-bit form of a matrix: (codes, scales), unpacked.
+
+    Not on the pages: the Open Compute Project's microscaling format with
+    e2m1 elements, 32 values along ``axis`` (1: a row, 0: a column) sharing the
+    scale 2^(b - 127).  b - 127 = floor(log2 max|v|) - 2, not below -127; each
+    value divided by the scale goes to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4,
+    6 (ties to the even code), saturating at 6.  codes [rows, cols] in 0..15
+    (bit 3: sign), scales [rows, cols / 32] or [rows / 32, cols].  A block
+    with a NaN or Inf has b = 255 and codes 0.
+    """
+    a = np.asarray(x, dtype=np.float64)
+    rows, cols = a.shape
+    b = _mx4_blocks(a, axis)
+    finite = np.all(np.isfinite(b), axis=1)
+    b = np.where(finite[:, None], b, 0.0)
+    top = np.max(np.abs(b), axis=1)
+    _, e = np.frexp(top)  # top = m 2^e with 0.5 <= m < 1: floor(log2) = e - 1
+    e = np.where(top > 0, np.maximum(e - 1 - 2, -127), -127)
+    q = np.abs(np.ldexp(b, -e[:, None]))
+    # distance to each grid value; among equal distances the even code wins
+    dist = np.abs(q[:, :, None] - E2M1[None, None, :])
+    near = dist == dist.min(axis=2, keepdims=True)
+    order = np.array([0, 2, 4, 6, 1, 3, 5, 7])
+    code = order[np.argmax(near[:, :, order], axis=2)]
+    code = code + 8 * np.signbit(b)
+    code[~finite] = 0
+    scale = np.where(finite, e + 127, 255)
+    if axis == 1:
+        return code.reshape(rows, cols), scale.reshape(rows, cols // 32)
+    return code.reshape(cols, rows).T, scale.reshape(cols, rows // 32).T
+
+
+def mx4_values(codes, scales, axis: int) -> np.ndarray:
+    """The values that unpacked codes and scale bytes stand for."""
+    codes = np.asarray(codes)
+    scales = np.asarray(scales).astype(np.int64)
+    v = E2M1[codes & 7] * np.where(codes & 8, -1.0, 1.0)
+    s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales - 127))
+    return v * np.repeat(s, 32, axis=axis)
