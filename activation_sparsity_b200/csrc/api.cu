@@ -179,7 +179,7 @@ int make_layout_uncached(int M, int d_in, int d_out, int K, Layout* L) {
     L->ucount = take(4);
     L->coef_hl = take((size_t)2 * M * d_in * 2);  // the tensor-core path's coefficient rows
   }
-  if (d_in % LAROSA_MX4_BLOCK == 0) L->mx4 = take(larosa::mx4_rows_buffer_bytes(M, d_in));
+  if (d_in % LAROSA_MX4_BLOCK == 0 && d_out % LAROSA_MX4_BLOCK == 0) L->mx4 = take(larosa::mx4_rows_buffer_bytes(M, d_in, d_out));
   L->total = off;
   return LAROSA_OK;
 }
@@ -1056,7 +1056,8 @@ int larosa_mx4_sparse_linear(const int32_t* idx, const float* val, int M, int K,
   const bool list = M == 1 && K > 0;  // one token's list is read by the product's CTAs themselves
   if (!list) e = larosa::launch_mx4_coef(idx, val, M, K, d_in, buf, dev_status, s);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit coefficient kernel");
-  e = larosa::launch_mx4_rows(list ? idx : nullptr, val, K, buf, M, W_codes, W_scales, d_in, d_out, y, dev_status, s);
+  e = larosa::launch_mx4_rows(list ? idx : nullptr, val, K, buf, reinterpret_cast<unsigned*>(at(ws, kOffTickets)), M,
+                              W_codes, W_scales, d_in, d_out, y, dev_status, s);
   return e == cudaSuccess ? LAROSA_OK : cuda_fail(e, "4-bit sparse linear kernel");
 }
 
@@ -1080,7 +1081,8 @@ int larosa_mx4_topk_linear(const float* x_rot, const void* W_codes, const void* 
   void* buf = at(ws, L.mx4);
   cudaError_t e = larosa::launch_topk(x_rot, M, d_in, K, idx, val, dev_status, s, nullptr, buf);
   if (e != cudaSuccess) return cuda_fail(e, "topk kernel");
-  e = larosa::launch_mx4_rows(nullptr, nullptr, K, buf, M, W_codes, W_scales, d_in, d_out, y, dev_status, s);
+  e = larosa::launch_mx4_rows(nullptr, nullptr, K, buf, reinterpret_cast<unsigned*>(at(ws, kOffTickets)), M, W_codes,
+                              W_scales, d_in, d_out, y, dev_status, s);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit sparse linear kernel");
   return check_workspace_lists(M, d_in, d_out, K, ws, dev_status, stream);
 }

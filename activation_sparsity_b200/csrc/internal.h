@@ -281,14 +281,16 @@ cudaError_t launch_mx4_dequantize(const void* codes, const void* scales, int row
 // token's kept list (idx not null, M = 1) or in `buf`
 // (mx4_rows_buffer_bytes): dense fp32 rows [M x d_in], or from 5 tokens on
 // (mx4_rows_take_operand) the tensor-core operand mx4_rows_operand describes.
-// launch_mx4_coef fills `buf` from kept lists; so does launch_topk.
+// launch_mx4_coef fills `buf` from kept lists; so does launch_topk.  The rest
+// of `buf` takes the splits' partial sums; `tickets` is a word per column
+// tile (at most 512), zero before and after.
 bool mx4_rows_take_operand(int M);
-size_t mx4_rows_buffer_bytes(int M, int d_in);
+size_t mx4_rows_buffer_bytes(int M, int d_in, int d_out);
 mx4::Operand mx4_rows_operand(void* buf, int M, int d_in);
 cudaError_t launch_mx4_coef(const int32_t* idx, const float* val, int M, int K, int d_in, void* buf,
                             int* dev_status, cudaStream_t stream);
-cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, const void* buf, int M, const void* codes,
-                            const void* scales, int d_in, int d_out, float* y, int* dev_status,
+cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, void* buf, unsigned* tickets, int M,
+                            const void* codes, const void* scales, int d_in, int d_out, float* y, int* dev_status,
                             cudaStream_t stream);
 
 }  // namespace larosa

@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(kQThreads)
 
 // The eight values of a code word, not yet scaled.
 __device__ __forceinline__ void code_values(uint32_t code, float (&v)[8]) {
-  uint32_t h[4];
-  mx4::e2m1_to_f16(code, h);
+  const uint32_t h[4] = {mx4::e2m1_to_f16<0>(code), mx4::e2m1_to_f16<1>(code), mx4::e2m1_to_f16<2>(code),
+                         mx4::e2m1_to_f16<3>(code)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = mx4::f16x2_to_f32(h[i]);

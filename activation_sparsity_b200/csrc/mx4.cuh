@@ -22,17 +22,17 @@ namespace mx4 {
 
 constexpr int kBlock = 32;
 
-// The four bytes of w, two e2m1 values each, as four f16 pairs (low half of
-// the byte in the low half of the pair).
-__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
+// Byte q of w, two e2m1 values, as an f16 pair (the low half of the byte in
+// the low half of the pair).
+template <int q>
+__device__ __forceinline__ uint32_t e2m1_to_f16(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b<4>;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}"
+      : "=r"(h)
+      : "r"(w), "n"(q));
+  return h;
 }
 
 // Two fp32 values to one byte of e2m1 codes, `lo` in the low half; nearest

@@ -26,36 +26,63 @@ __device__ __forceinline__ void split_pieces(float v, __half* p0, __half* p1) {
   *p1 = __float2half_rn((v - __half2float(*p0)) * 2048.f);
 }
 
-// D = A B + C, A 16 x 16 and B 16 x 8 of f16, D and C fp32.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint2 b) {
+// D = A B, or D += A B, with A 16 x 16 and B 16 x 8 of f16, D fp32.
+__device__ __forceinline__ void mma_f16(float (&d)[4], bool fresh, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint2 b) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(fresh ? 0.f : d[0]), "f"(fresh ? 0.f : d[1]),
+        "f"(fresh ? 0.f : d[2]), "f"(fresh ? 0.f : d[3]));
+}
+// The same with a reduction of 8: A 16 x 8, B 8 x 8.
+__device__ __forceinline__ void mma_f16_k8(float (&d)[4], bool fresh, uint32_t a0, uint32_t a1, uint32_t b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %8, %9, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b), "f"(fresh ? 0.f : d[0]), "f"(fresh ? 0.f : d[1]), "f"(fresh ? 0.f : d[2]),
+        "f"(fresh ? 0.f : d[3]));
 }
 
-// One lane's part of a block: 16 columns of its four rows of both 16-row
-// steps, and the columns' scale bytes.
+// A block of 32 rows by 128 columns in shared memory, as a warp's copies
+// leave it: the rows of both steps (position 16 step + 4 i + t holds row i of
+// the lanes t, so that a warp reads 256 contiguous bytes for each i) and the
+// columns' scale bytes.
+struct __align__(16) Tile {
+  uint8_t row[32][64];
+  uint8_t scale[128];
+};
+
+// One lane's part of a tile: 16 columns of its rows of both steps (four of
+// a 16-row step, two of an 8-row one), and the columns' scale bytes.
 struct RowSet {
   uint2 w[2][4];
   uint4 s;
 
-  // Row row(step, i) of the block (255: none, read as zeros).  base points
-  // at this lane's columns of the block's first row, scales at the block's.
-  template <typename Row>
-  __device__ __forceinline__ void load(const uint8_t* base, size_t row_bytes, const uint8_t* scales, bool any,
-                                       Row row) {
+  template <int R0, int R1>
+  __device__ __forceinline__ void read(const Tile& tile, int g, int t) {
 #pragma unroll
-    for (int step = 0; step < 2; ++step)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t r = row(step, i);
-        w[step][i] = r < 32u ? __ldcs(reinterpret_cast<const uint2*>(base + r * row_bytes)) : make_uint2(0u, 0u);
-      }
-    s = any ? __ldg(reinterpret_cast<const uint4*>(scales)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 4; ++i) {
+      if (i < R0) w[0][i] = *reinterpret_cast<const uint2*>(&tile.row[4 * i + t][8 * g]);
+      if (i < R1) w[1][i] = *reinterpret_cast<const uint2*>(&tile.row[16 + 4 * i + t][8 * g]);
+    }
+    s = *reinterpret_cast<const uint4*>(&tile.scale[16 * g]);
   }
 };
+
+// Asynchronous copies of 16 bytes to shared memory, through L2 only
+// (weights) or also L1 (operands that other warps of the SM read too).
+__device__ __forceinline__ void copy16_l2(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_l1(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `pending` of this thread's latest groups are in flight.
+template <int pending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(pending) : "memory");
+}
 
 // The A operands of one 8-column half: E pairs the even columns of two rows,
 // O the odd ones (column 2 q in byte q).
@@ -65,51 +92,62 @@ __device__ __forceinline__ void pair_rows(uint32_t r0, uint32_t r1, uint32_t* ev
   *odd = ((r0 >> 4) & kLow) | (r1 & ~kLow);
 }
 
+// Column pair q of one 8-column half: the steps' products into a fresh
+// accumulator, then the scales into acc.  w[step]: e01, o01, e23, o23.
+template <int NT, int R0, int R1, int q>
+__device__ __forceinline__ void column_pair(const uint32_t (&w)[2][4], uint32_t scales, const uint2 (&b)[2][NT],
+                                            const float (&sx)[NT], float (&acc)[NT][8][2], int at) {
+  float d[NT][4];
+#pragma unroll
+  for (int step = 0; step < 2; ++step) {
+    const int R = step == 0 ? R0 : R1;
+    if (R == 0) continue;
+    const uint32_t a0 = e2m1_to_f16<q>(w[step][0]), a1 = e2m1_to_f16<q>(w[step][1]);
+    if (R == 4) {
+      const uint32_t a2 = e2m1_to_f16<q>(w[step][2]), a3 = e2m1_to_f16<q>(w[step][3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(d[n], step == 0, a0, a1, a2, a3, b[step][n]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16_k8(d[n], step == 0, a0, a1, b[step][n].x);
+    }
+  }
+  float s0, s1;
+  scale_pair(q & 1 ? scales >> 16 : scales & 0xffffu, &s0, &s1);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    // d[0], d[1]: the two pieces of column 2 q; d[2], d[3] of column 2 q + 1
+    acc[n][at][0] += fmaf(d[n][1], 0x1p-11f, d[n][0]) * sx[n] * s0;
+    acc[n][at][1] += fmaf(d[n][3], 0x1p-11f, d[n][2]) * sx[n] * s1;
+  }
+}
+
 // acc[n][q][h] += (block product of token 4 n + t and column 2 q + h of the
-// lane's 16): one or two 16-row steps into fresh accumulators, then the
-// scales.  b[step][n] is the lane's B operand, sx[n] its token's scale.
-template <int NT>
-__device__ __forceinline__ void block_product(const RowSet& rs, bool two, const uint2 (&b)[2][NT],
-                                              const float (&sx)[NT], float (&acc)[NT][8][2]) {
+// lane's 16): steps of R0 and R1 rows per lane (4: 16 rows, 2: 8 rows, 0:
+// none) into fresh accumulators, then the scales.  b[step][n] is the lane's B
+// operand (.x alone for an 8-row step), sx[n] its token's scale.
+template <int NT, int R0, int R1>
+__device__ __forceinline__ void block_product(const RowSet& rs, const uint2 (&b)[2][NT], const float (&sx)[NT],
+                                              float (&acc)[NT][8][2]) {
   const uint32_t sw[4] = {rs.s.x, rs.s.y, rs.s.z, rs.s.w};
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    // [step][e01, o01, e23, o23][column pair]
-    uint32_t a[2][4][4];
+    uint32_t w[2][4];
 #pragma unroll
     for (int step = 0; step < 2; ++step) {
-      if (step == 1 && !two) break;
-      uint32_t r[4], e01, o01, e23, o23;
+      const int R = step == 0 ? R0 : R1;
+      if (R == 0) continue;
+      uint32_t r[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = half == 0 ? rs.w[step][i].x : rs.w[step][i].y;
-      pair_rows(r[0], r[1], &e01, &o01);
-      pair_rows(r[2], r[3], &e23, &o23);
-      e2m1_to_f16(e01, a[step][0]);
-      e2m1_to_f16(o01, a[step][1]);
-      e2m1_to_f16(e23, a[step][2]);
-      e2m1_to_f16(o23, a[step][3]);
+      for (int i = 0; i < 4; ++i)
+        if (i < R) r[i] = half == 0 ? rs.w[step][i].x : rs.w[step][i].y;
+      pair_rows(r[0], r[1], &w[step][0], &w[step][1]);
+      if (R == 4) pair_rows(r[2], r[3], &w[step][2], &w[step][3]);
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float d[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-        mma_f16(d[n], a[0][0][q], a[0][1][q], a[0][2][q], a[0][3][q], b[0][n]);
-      }
-      if (two) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(d[n], a[1][0][q], a[1][1][q], a[1][2][q], a[1][3][q], b[1][n]);
-      }
-      float s0, s1;
-      scale_pair(q & 1 ? sw[2 * half + q / 2] >> 16 : sw[2 * half + q / 2] & 0xffffu, &s0, &s1);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        // d[0], d[1]: the two pieces of column 2 q; d[2], d[3] of column 2 q + 1
-        acc[n][4 * half + q][0] += fmaf(d[n][1], 0x1p-11f, d[n][0]) * sx[n] * s0;
-        acc[n][4 * half + q][1] += fmaf(d[n][3], 0x1p-11f, d[n][2]) * sx[n] * s1;
-      }
-    }
+    column_pair<NT, R0, R1, 0>(w, sw[2 * half], b, sx, acc, 4 * half);
+    column_pair<NT, R0, R1, 1>(w, sw[2 * half], b, sx, acc, 4 * half + 1);
+    column_pair<NT, R0, R1, 2>(w, sw[2 * half + 1], b, sx, acc, 4 * half + 2);
+    column_pair<NT, R0, R1, 3>(w, sw[2 * half + 1], b, sx, acc, 4 * half + 3);
   }
 }
 

@@ -28,28 +28,34 @@
 //   * a block's product is a fresh accumulator, scaled by the two powers of
 //     two (the token's and the column's) when it is added to the fp32 sum.
 //
-// A warp takes a block of 32 rows by 128 columns (64-byte row segments: a
-// lane's 16 columns are 8 bytes) and loads the next block while it multiplies
-// this one.  A CTA's eight warps take the blocks of one split in turn and add
-// their sums in warp order through shared memory; the splits of a column
-// tile are a thread-block cluster whose CTAs add their tiles through
-// distributed shared memory in rank order, so the result does not depend on
-// timing.
+// A warp takes a block of 32 rows by 128 columns (64-byte row segments).  Its
+// rows arrive by asynchronous 16-byte copies in the warp's own ring of shared
+// memory tiles, two blocks ahead: a block is about 250 instructions, less
+// than the latency of its rows, and registers for more than one block in
+// flight would halve the warps an SM holds.  Every copy is unconditional: an
+// empty slot names a row of the block that is read anyway (its coefficient is
+// zero), and columns past the matrix name the last ones (their sums are not
+// written).  A CTA's eight warps take the blocks of one split in turn and add
+// their sums in warp order through shared memory.  The splits of a column
+// tile write their sums to the workspace, and the last one to arrive adds
+// them in split order, so the result does not depend on timing.  (As
+// thread-block clusters with distributed shared memory the splits left SMs
+// empty: of clusters of seven, one CTA per SM, 15 fit the GPU at a time.)
 //
 // Two ways to the B operand, by the number of tokens:
-//   up to 4 tokens   every warp makes the operand of its own block from the
-//                    tokens' fp32 coefficients (a kept list scattered into
-//                    shared memory by the CTA, or dense rows in global
-//                    memory) and packs the rows some token keeps into as few
-//                    16-row steps as they fill;
-//   5 to 16 tokens   the operand is made once, by one CTA per token, and read
-//                    through L1 by two warps side by side (256 columns per
-//                    CTA): making it in every column tile would cost as much
-//                    as the product.  Nearly every row is kept by some token,
-//                    so rows are not packed, only left unread where no token
-//                    keeps them.
-#include <cooperative_groups.h>
-
+//   up to 4 tokens   the CTA makes the operands of its split's blocks in
+//                    shared memory from the tokens' fp32 coefficients (a kept
+//                    list it scatters itself, or dense rows in global memory)
+//                    and packs the rows some token keeps into steps of 16 and
+//                    8 rows: at 60 % kept a block takes 24 of 32 slots.  One
+//                    or two warps abreast (128 or 256 columns per CTA) share
+//                    them;
+//   5 to 16 tokens   the operand is made once, by one CTA per token, and
+//                    copied along with the rows: making it in every column
+//                    tile would cost as much as the product.  Nearly every
+//                    row is kept by some token, so rows are not packed; one
+//                    that no token keeps is replaced by one that is read
+//                    anyway.
 #include <algorithm>
 
 #include "common.cuh"
@@ -57,14 +63,16 @@
 #include "mx4.cuh"
 #include "mx4_mma.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace larosa {
 namespace {
 
 constexpr int kRThreads = 256;
 constexpr int kRWarps = kRThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kRing = 3;      // tiles of a warp's ring, 5 to 16 tokens
+constexpr int kFewRing = 3;   // up to 4 tokens
+constexpr int kFewCtas = 3;   // CTAs per SM, up to 4 tokens
+constexpr int kManyCtas = 2;  // 5 to 16 tokens
+constexpr int kMaxSplits = 16;
 constexpr int kMaxSplitRows = 16384;  // rows of one split a kept list is scattered into
 
 struct RParams {
@@ -75,18 +83,21 @@ struct RParams {
   const uint8_t* codes;
   const uint8_t* scales;
   float* y;
+  float* partials;    // [splits][tile][M][columns of a tile]
+  unsigned* tickets;  // a word per tile, zero between calls
   int M, K, d_in, d_out;
   int blocks_per_split;
   int* dev_status;
 };
 
-// The CTA's sums of every warp, added in warp order, then over the cluster in
-// rank order, to y.  Warp w holds columns (w % kHalves) 128 ... of the tile.
+// The CTA's sums of every warp, added in warp order, then those of the tile's
+// splits in split order, to y.  Warp w holds columns (w % kHalves) 128 ... of
+// the tile.
 template <int NT, int kHalves>
 __device__ __forceinline__ void reduce_tile(const float (&acc)[NT][8][2], float* part, const RParams& p) {
   constexpr int kTok = 4 * NT;
   constexpr int kCols = 128 * kHalves;
-  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ unsigned s_order;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   // [block lane][token][column]
@@ -97,172 +108,272 @@ __device__ __forceinline__ void reduce_tile(const float (&acc)[NT][8][2], float*
     for (int q = 0; q < 8; ++q)
       *reinterpret_cast<float2*>(mine + (size_t)4 * n * kCols + 2 * q) = make_float2(acc[n][q][0], acc[n][q][1]);
   __syncthreads();
-  for (int e = tid; e < p.M * kCols; e += kRThreads) {
+  const int S = gridDim.x, tile = blockIdx.y, count = p.M * kCols;
+  float* slab = p.partials + ((size_t)blockIdx.x * gridDim.y + tile) * count;
+  for (int e = tid; e < count; e += kRThreads) {
     float s = part[e];
 #pragma unroll
     for (int w = 1; w < kRWarps / kHalves; ++w) s += part[w * kTok * kCols + e];
-    part[e] = s;  // this thread's own element: no other reads it before the barrier
+    if (S > 1) {
+      __stcg(slab + e, s);
+    } else {
+      const int m = e / kCols, j = tile * kCols + e % kCols;
+      if (j < p.d_out) p.y[(size_t)m * p.d_out + j] = s;
+    }
   }
-  const int R = static_cast<int>(cluster.num_blocks());
-  if (R > 1)
-    cluster.sync();
-  else
-    __syncthreads();
-  const int q0 = blockIdx.x * kCols / R, width = (blockIdx.x + 1) * kCols / R - q0;
-  for (int e = tid; e < p.M * width; e += kRThreads) {
-    const int m = e / width, c = q0 + e % width;
-    const int j = blockIdx.y * kCols + c;
+  if (S == 1) return;
+  __syncthreads();
+  if (tid == 0) s_order = atomic_add_acq_rel_gpu(&p.tickets[tile], 1u);
+  __syncthreads();
+  if (s_order != (unsigned)S - 1u) return;
+  const size_t step = (size_t)gridDim.y * count;
+  for (int e = tid; e < count; e += kRThreads) {
+    const float* from = p.partials + (size_t)tile * count + e;
     float s = 0.f;
-    for (int r = 0; r < R; ++r) s += cluster.map_shared_rank(part, r)[m * kCols + c];
+    for (int r0 = 0; r0 < S; r0 += 8) {  // eight loads in flight, added in split order
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = r0 + i < S ? __ldcg(from + (size_t)(r0 + i) * step) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    const int m = e / kCols, j = tile * kCols + e % kCols;
     if (j < p.d_out) p.y[(size_t)m * p.d_out + j] = s;
   }
-  if (R > 1) cluster.sync();  // no CTA leaves while another may still read its tile
+  if (tid == 0) p.tickets[tile] = 0u;  // every split has arrived
 }
 
-// A warp's packed operand of one block, up to four tokens.
-struct __align__(16) Packed {
-  __half piece[2][8][16];  // [step][2 token + piece][slot]
-  uint8_t row[32];         // row of each slot, 255 beyond the kept ones
-  float sx[4];
-};
+// Copies of a block's tile by one warp: `count` positions (a multiple of 8)
+// of 64 bytes, four lanes each, and the scales.  row(p) is the byte offset of
+// position p's row from `base`; lane chunks lie `chunk` bytes into a row.
+template <typename Row>
+__device__ __forceinline__ void copy_tile(mx4::Tile& tile, const uint8_t* base, uint32_t chunk, int count,
+                                          const uint8_t* scales, int lane, Row row) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (8 * j < count) {
+      const int pos = 8 * j + (lane >> 2);
+      mx4::copy16_l2(&tile.row[pos][16 * (lane & 3)], base + row(pos) + chunk);
+    }
+  if (lane < 8) mx4::copy16_l2(&tile.scale[16 * lane], scales);
+}
 
 // ---------------------------------------------------------------- up to 4 tokens
 
-template <bool kList>
-__global__ void __launch_bounds__(kRThreads, 2) mx4_rows_few_kernel(const RParams p) {
+// A block's packed operand for up to kM tokens.
+template <int kM>
+struct __align__(16) Packed {
+  __half piece[2][2 * kM][16];  // [step][2 token + piece][slot]
+  uint32_t off[32];        // byte offset of each tile position's row from the block's first row
+  float sx[4];
+  int n;  // slots in use
+  int pad[3];
+};
+
+// Tile position of a slot when n are in use: 16-row steps hold row 4 t + i of
+// the step at 4 i + t, 8-row ones (the rest fits eight) row 2 t + i.
+__device__ __forceinline__ int position_of(int slot, int n) {
+  const int s = slot & 15;
+  const bool eight = slot < 16 ? n <= 8 : n <= 24;
+  if (!eight) return (slot & 16) + (s & 3) * 4 + (s >> 2);
+  return (slot & 16) + (s < 8 ? (s & 1) * 4 + (s >> 1) : s);
+}
+
+template <int kM>
+struct FewSmem {
+  static constexpr size_t kRingBytes = sizeof(mx4::Tile) * kFewRing * kRWarps;
+  static constexpr size_t kChunk = kM == 1 ? 48 : 32;  // blocks packed at a time
+  static constexpr size_t kBytes = kRingBytes + kChunk * sizeof(Packed<kM>);
+  static_assert((size_t)kRWarps * 4 * 128 * 4 <= kRingBytes, "the sums reuse the rings");
+};
+
+// kM: 1 for one token, 4 for two to four.
+template <bool kList, int kM, int kHalves>
+__global__ void __launch_bounds__(kRThreads, kFewCtas) mx4_rows_few_kernel(const RParams p) {
+  constexpr int kLanes = kRWarps / kHalves;
+  constexpr int kFewChunk = (int)FewSmem<kM>::kChunk;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ Packed s_op[kRWarps][2];
-  float* stage = reinterpret_cast<float*>(smem);  // kList: the split's coefficients
+  Packed<kM>* ops = reinterpret_cast<Packed<kM>*>(smem + FewSmem<kM>::kRingBytes);
+  float* stage = reinterpret_cast<float*>(smem + FewSmem<kM>::kBytes);  // kList: the split's coefficients
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
+  // this lane's column of the B operand; with one token only two exist, and
+  // the others' products are never added
+  const int gb = g % (2 * kM);
+  mx4::Tile* ring = reinterpret_cast<mx4::Tile*>(smem) + warp * kFewRing;
   const int n_blocks = p.d_in / mx4::kBlock;
   const int b_begin = blockIdx.x * p.blocks_per_split;
   const int b_end = min(n_blocks, b_begin + p.blocks_per_split);
-  const int col = blockIdx.y * 128 + g * 16;  // this lane's 16 columns
-  const bool in = col < p.d_out;
-  const size_t row_bytes = (size_t)p.d_out / 2;
+  const int col0 = (int)blockIdx.y * 128 * kHalves + (warp % kHalves) * 128;
+  const uint32_t row_bytes = (uint32_t)p.d_out / 2;
+  // this lane's copies: 16 bytes of rows and of scales, the last ones where
+  // they lie past the matrix
+  const uint32_t chunk = min((uint32_t)col0 / 2 + 16u * (lane & 3), row_bytes - 16u);
+  const uint8_t* s_col = p.scales + min(col0 + 16 * lane, p.d_out - 16);
 
   float acc[1][8][2];
 #pragma unroll
   for (int q = 0; q < 8; ++q) acc[0][q][0] = acc[0][q][1] = 0.f;
 
   if constexpr (kList) {
-    const int rows = (b_end - b_begin) * 32;
+    const int rows = max(b_end - b_begin, 0) * 32;
     for (int i = tid; i < rows / 4; i += kRThreads)
       reinterpret_cast<float4*>(stage)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     bool bad = false;
-    for (int i = tid; i < p.K; i += kRThreads) {
-      const unsigned r = (unsigned)__ldg(p.idx + i);
-      const float v = __ldg(p.val + i);
-      if (r - (unsigned)b_begin * 32u < (unsigned)max(rows, 0) && r < (unsigned)p.d_in)
-        stage[r - b_begin * 32] = v;
-      bad |= r >= (unsigned)p.d_in;
+    const unsigned first = (unsigned)b_begin * 32u;
+    constexpr int kBatch = 8;  // entries in flight per thread
+    for (int i0 = tid; i0 < p.K; i0 += kBatch * kRThreads) {
+      unsigned r[kBatch];
+      float v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kRThreads;
+        r[k] = i < p.K ? (unsigned)__ldg(p.idx + i) : first;
+        v[k] = i < p.K ? __ldg(p.val + i) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i0 + k * kRThreads >= p.K) break;
+        if (r[k] - first < (unsigned)rows) stage[r[k] - first] = v[k];
+        bad |= r[k] >= (unsigned)p.d_in;
+      }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.dev_status, LAROSA_DEV_INDEX);
-    __syncthreads();
   } else {
     pdl_wait();
     pdl_launch_dependents();
   }
 
-  // coefficient of row `lane` of block b for token m
-  auto coef = [&](int b, int m) -> float {
-    if constexpr (kList) return stage[(b - b_begin) * 32 + lane];
-    return __ldg(p.coef + (size_t)m * p.d_in + b * 32 + lane);
-  };
-  constexpr int kM = kList ? 1 : 4;
-  float v[kM];
-  auto read_coef = [&](int b) {
+  for (int c0 = b_begin; c0 < b_end; c0 += kFewChunk) {
+    const int nb = min(kFewChunk, b_end - c0);
+    __syncthreads();  // the list is staged; the chunk before is used up
+    // all of a warp's coefficients are loaded before the first is used
+    constexpr int kPer = kFewChunk / kRWarps;
+    float vs[kPer][kM];
 #pragma unroll
-    for (int m = 0; m < kM; ++m) v[m] = b < b_end && m < p.M ? coef(b, m) : 0.f;
-  };
-  // packs block b's coefficients (in v) into `o`; returns the kept count
-  auto pack = [&](Packed& o) -> int {
-    bool any = false;
+    for (int i = 0; i < kPer; ++i) {
+      const int b = warp + i * kRWarps;
 #pragma unroll
-    for (int m = 0; m < kM; ++m) any |= v[m] != 0.f;  // a coefficient of zero adds nothing
-    const unsigned kept = __ballot_sync(0xffffffffu, any);
-    const unsigned below = (1u << lane) - 1u;
-    const int n_kept = __popc(kept);
-    const int slot = any ? __popc(kept & below) : n_kept + __popc(~kept & below);
-    __syncwarp();
-#pragma unroll
-    for (int m = 0; m < kM; ++m) {
-      if (m < p.M) {
-        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[m]) & 0x7fffffffu);
-        float up, down;
-        mx4::piece_scale(top, &up, &down);
-        __half p0, p1;
-        mx4::split_pieces(v[m] * up, &p0, &p1);
-        o.piece[slot >> 4][2 * m][slot & 15] = p0;
-        o.piece[slot >> 4][2 * m + 1][slot & 15] = p1;
-        if (lane == 0) o.sx[m] = down;
+      for (int m = 0; m < kM; ++m) {
+        if constexpr (kList)
+          vs[i][m] = b < nb ? stage[(c0 - b_begin + b) * 32 + lane] : 0.f;
+        else
+          vs[i][m] = b < nb && m < p.M ? __ldg(p.coef + (size_t)m * p.d_in + (c0 + b) * 32 + lane) : 0.f;
       }
     }
-    o.row[slot] = any ? (uint8_t)lane : (uint8_t)255;
-    __syncwarp();
-    return n_kept;
-  };
-  auto fetch = [&](int b, const Packed& o, int n_kept, mx4::RowSet& rs) {
-    rs.load(p.codes + (size_t)b * 32 * row_bytes + (col >> 1), row_bytes, p.scales + (size_t)b * p.d_out + col,
-            in && n_kept > 0, [&](int step, int i) {
-              const uint32_t r = *reinterpret_cast<const uint32_t*>(&o.row[16 * step + 4 * t]);
-              return in ? (r >> (8 * i)) & 255u : 255u;
-            });
-  };
-
-  mx4::RowSet cur, next;
-  int n_cur = 0, n_next = 0, buf = 0;
-  int b = b_begin + warp;
-  if (b < b_end) {
-    read_coef(b);
-    n_cur = pack(s_op[warp][0]);
-    fetch(b, s_op[warp][0], n_cur, cur);
-    read_coef(b + kRWarps);
-  }
-  for (; b < b_end; b += kRWarps) {
-    if (b + kRWarps < b_end) {
-      n_next = pack(s_op[warp][buf ^ 1]);
-      fetch(b + kRWarps, s_op[warp][buf ^ 1], n_next, next);
-      read_coef(b + 2 * kRWarps);
-    }
-    if (n_cur > 0) {
-      const Packed& o = s_op[warp][buf];
-      uint2 bop[2][1];
 #pragma unroll
-      for (int step = 0; step < 2; ++step) bop[step][0] = *reinterpret_cast<const uint2*>(&o.piece[step][g][4 * t]);
-      const float sx[1] = {o.sx[t]};
-      mx4::block_product<1>(cur, n_cur > 16, bop, sx, acc);
+    for (int i = 0; i < kPer; ++i) {
+      const int b = warp + i * kRWarps;
+      if (b >= nb) break;
+      Packed<kM>& o = ops[b];
+      const float(&v)[kM] = vs[i];
+      bool any = false;
+#pragma unroll
+      for (int m = 0; m < kM; ++m) any |= v[m] != 0.f;  // a coefficient of zero adds nothing
+      const unsigned kept = __ballot_sync(0xffffffffu, any);
+      const unsigned below = (1u << lane) - 1u;
+      const int n_kept = __popc(kept);
+      const int slot = any ? __popc(kept & below) : n_kept + __popc(~kept & below);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        if (m < p.M) {
+          const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[m]) & 0x7fffffffu);
+          float up, down;
+          mx4::piece_scale(top, &up, &down);
+          __half p0, p1;
+          mx4::split_pieces(v[m] * up, &p0, &p1);
+          o.piece[slot >> 4][2 * m][slot & 15] = p0;
+          o.piece[slot >> 4][2 * m + 1][slot & 15] = p1;
+          if (lane == 0) o.sx[m] = down;
+        }
+      }
+      o.off[position_of(slot, n_kept)] = (any ? (uint32_t)lane : kept ? (uint32_t)__ffs(kept) - 1u : 0u) * row_bytes;
+      if (lane == 0) o.n = n_kept;
     }
-    cur = next;
-    n_cur = n_next;
-    buf ^= 1;
+    __syncthreads();
+
+    auto copy = [&](int b, int stage_no) {
+      if (b < nb) {
+        const Packed<kM>& o = ops[b];
+        const int n = o.n;
+        if (n > 0)
+          copy_tile(ring[stage_no], p.codes + (size_t)(c0 + b) * 32 * row_bytes, chunk, (n + 7) & ~7,
+                    s_col + (size_t)(c0 + b) * p.d_out, lane, [&](int pos) { return o.off[pos]; });
+      }
+      mx4::copies_commit();
+    };
+    int b = warp / kHalves;
+#pragma unroll
+    for (int s = 0; s < kFewRing - 1; ++s) copy(b + s * kLanes, s);
+    for (int it = 0; b < nb; b += kLanes, ++it) {
+      __syncwarp();  // every lane has read the tile that is filled next
+      copy(b + (kFewRing - 1) * kLanes, (it + kFewRing - 1) % kFewRing);
+      mx4::copies_wait<kFewRing - 1>();
+      __syncwarp();  // the other lanes' copies too
+      const Packed<kM>& o = ops[b];
+      const int n = o.n;
+      if (n == 0) continue;
+      const mx4::Tile& tile = ring[it % kFewRing];
+      const float sx[1] = {o.sx[kM == 1 ? 0 : t]};
+      mx4::RowSet rs;
+      uint2 bop[2][1];
+      if (n <= 8) {
+        rs.read<2, 0>(tile, g, t);
+        bop[0][0] = make_uint2(*reinterpret_cast<const uint32_t*>(&o.piece[0][gb][2 * t]), 0u);
+        mx4::block_product<1, 2, 0>(rs, bop, sx, acc);
+        continue;
+      }
+      bop[0][0] = *reinterpret_cast<const uint2*>(&o.piece[0][gb][4 * t]);
+      if (n <= 16) {
+        rs.read<4, 0>(tile, g, t);
+        mx4::block_product<1, 4, 0>(rs, bop, sx, acc);
+      } else if (n <= 24) {
+        rs.read<4, 2>(tile, g, t);
+        bop[1][0] = make_uint2(*reinterpret_cast<const uint32_t*>(&o.piece[1][gb][2 * t]), 0u);
+        mx4::block_product<1, 4, 2>(rs, bop, sx, acc);
+      } else {
+        rs.read<4, 4>(tile, g, t);
+        bop[1][0] = *reinterpret_cast<const uint2*>(&o.piece[1][gb][4 * t]);
+        mx4::block_product<1, 4, 4>(rs, bop, sx, acc);
+      }
+    }
+    mx4::copies_wait<0>();
   }
   __syncthreads();
   // lanes of tokens that do not exist hold whatever their columns held; only
   // tokens below M are added
-  reduce_tile<1, 1>(acc, reinterpret_cast<float*>(smem), p);
+  reduce_tile<1, kHalves>(acc, reinterpret_cast<float*>(smem), p);
 }
 
 // ---------------------------------------------------------------- 5 to 16 tokens
 
+// A tile and its block's operand and token scales.
 template <int NT>
-__global__ void __launch_bounds__(kRThreads, NT == 2 ? 2 : 1) mx4_rows_many_kernel(const RParams p) {
+struct __align__(16) ManyTile {
+  mx4::Tile rows;
+  __half piece[2][NT][8][16];
+  float sx[4 * NT];
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kRThreads, kManyCtas) mx4_rows_many_kernel(const RParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int kTok = 4 * NT;
   constexpr int kHalves = 2, kLanes = kRWarps / kHalves;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
+  ManyTile<NT>* ring = reinterpret_cast<ManyTile<NT>*>(smem) + warp * kRing;
   const int n_blocks = p.d_in / mx4::kBlock;
   const int b_begin = blockIdx.x * p.blocks_per_split;
   const int b_end = min(n_blocks, b_begin + p.blocks_per_split);
-  const int col = blockIdx.y * 128 * kHalves + (warp % kHalves) * 128 + g * 16;
-  const bool in = col < p.d_out;
-  const size_t row_bytes = (size_t)p.d_out / 2;
+  const int col0 = (int)blockIdx.y * 128 * kHalves + (warp % kHalves) * 128;
+  const uint32_t row_bytes = (uint32_t)p.d_out / 2;
+  const uint32_t chunk = min((uint32_t)col0 / 2 + 16u * (lane & 3), row_bytes - 16u);
+  const uint8_t* s_col = p.scales + min(col0 + 16 * lane, p.d_out - 16);
 
   float acc[NT][8][2];
 #pragma unroll
@@ -278,38 +389,56 @@ __global__ void __launch_bounds__(kRThreads, NT == 2 ? 2 : 1) mx4_rows_many_kern
     const unsigned m = b < b_end && lane < p.M ? __ldg(p.op.mask + (size_t)b * kTok + lane) : 0u;
     return __reduce_or_sync(0xffffffffu, m);
   };
-  auto fetch = [&](int b, unsigned kept, mx4::RowSet& rs) {
-    const unsigned mine = in ? kept >> (4 * t) : 0u;
-    rs.load(p.codes + (size_t)b * 32 * row_bytes + (col >> 1), row_bytes, p.scales + (size_t)b * p.d_out + col,
-            in && kept != 0u, [&](int step, int i) {
-              return (mine >> (16 * step + i)) & 1u ? (uint32_t)(16 * step + 4 * t + i) : 255u;
-            });
+  auto copy = [&](int b, unsigned kept, int stage_no) {
+    if (kept != 0u) {
+      ManyTile<NT>& tile = ring[stage_no];
+      const uint32_t first = (uint32_t)__ffs(kept) - 1u;
+      copy_tile(tile.rows, p.codes + (size_t)b * 32 * row_bytes, chunk, 32, s_col + (size_t)b * p.d_out, lane,
+                [&](int pos) {
+                  const uint32_t r = (pos & 16) + (pos & 3) * 4 + ((pos >> 2) & 3);
+                  return ((kept >> r) & 1u ? r : first) * row_bytes;
+                });
+      const unsigned char* src = reinterpret_cast<const unsigned char*>(p.op.piece) + (size_t)b * (512 * NT);
+      unsigned char* dst = reinterpret_cast<unsigned char*>(tile.piece);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) mx4::copy16_l1(dst + 512 * i + 16 * lane, src + 512 * i + 16 * lane);
+      if (lane < NT) mx4::copy16_l1(&tile.sx[4 * lane], p.op.sx + (size_t)b * kTok + 4 * lane);
+    }
+    mx4::copies_commit();
   };
 
-  mx4::RowSet cur, next;
   int b = b_begin + warp / kHalves;
-  unsigned k_cur = kept_rows(b), k_next = kept_rows(b + kLanes);
-  if (b < b_end) fetch(b, k_cur, cur);
-  for (; b < b_end; b += kLanes) {
-    if (b + kLanes < b_end) fetch(b + kLanes, k_next, next);
-    const unsigned k_after = kept_rows(b + 2 * kLanes);
-    if (k_cur != 0u) {
+  // kept[s]: rows of the block in tile s of the ring, and of the one after
+  unsigned kept[kRing];
+#pragma unroll
+  for (int s = 0; s < kRing; ++s) kept[s] = kept_rows(b + s * kLanes);
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) copy(b + s * kLanes, kept[s], s);
+  for (int it = 0; b < b_end; b += kLanes, ++it) {
+    __syncwarp();  // every lane has read the tile that is filled next
+    copy(b + (kRing - 1) * kLanes, kept[kRing - 1], (it + kRing - 1) % kRing);
+    const unsigned after = kept_rows(b + kRing * kLanes);
+    mx4::copies_wait<kRing - 1>();
+    __syncwarp();  // the other lanes' copies too
+    if (kept[0] != 0u) {
+      const ManyTile<NT>& tile = ring[it % kRing];
+      mx4::RowSet rs;
+      rs.read<4, 4>(tile.rows, g, t);
       uint2 bop[2][NT];
       float sx[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int step = 0; step < 2; ++step)
-          bop[step][n] = __ldg(reinterpret_cast<const uint2*>(p.op.piece) +
-                               ((((size_t)b * 2 + step) * NT + n) * 8 + g) * 4 + t);
-        sx[n] = __ldg(p.op.sx + (size_t)b * kTok + 4 * n + t);
+        for (int step = 0; step < 2; ++step) bop[step][n] = *reinterpret_cast<const uint2*>(&tile.piece[step][n][g][4 * t]);
+        sx[n] = tile.sx[4 * n + t];
       }
-      mx4::block_product<NT>(cur, true, bop, sx, acc);
+      mx4::block_product<NT, 4, 4>(rs, bop, sx, acc);
     }
-    cur = next;
-    k_cur = k_next;
-    k_next = k_after;
+#pragma unroll
+    for (int s = 0; s < kRing - 1; ++s) kept[s] = kept[s + 1];
+    kept[kRing - 1] = after;
   }
+  mx4::copies_wait<0>();
   __syncthreads();
   reduce_tile<NT, kHalves>(acc, reinterpret_cast<float*>(smem), p);
 }
@@ -346,17 +475,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 }
 
-// CTAs per column tile: the count that ends the slowest CTA first when
-// `slots` CTAs run at a time, at most eight (the portable cluster size) and
-// at least one block per warp.
-int pick_cluster(int tiles, int n_blocks, int lanes, int slots) {
+// CTAs per column tile: the count that ends the last CTA first when `slots`
+// of them run at a time, at least one block per warp (`lanes` blocks at a
+// time).
+int pick_splits(int tiles, int n_blocks, int lanes, int slots) {
   int best = 1;
   double best_t = 1e30;
-  for (int S = 1; S <= kMaxCluster; S *= 2) {
+  for (int S = 1; S <= kMaxSplits; ++S) {
     if (S > 1 && n_blocks < S * lanes) break;
-    const double waves = std::max(1.0, (double)((long long)tiles * S) / slots);
+    const long long waves = ((long long)tiles * S + slots - 1) / slots;
     const int per_warp = ((n_blocks + S - 1) / S + lanes - 1) / lanes;
-    const double t = waves * (per_warp + 3.0);  // 3: the CTA's fixed work, in blocks
+    const double t = (double)waves * (per_warp + 3.0);  // 3: the CTA's fixed work, in blocks
     if (t < best_t * 0.999) {
       best_t = t;
       best = S;
@@ -365,7 +494,8 @@ int pick_cluster(int tiles, int n_blocks, int lanes, int slots) {
   return best;
 }
 
-// Raises a kernel's dynamic shared memory limit, once per device.
+// Raises a kernel's dynamic shared memory limit, once per device, and gives
+// it all of the unified L1 / shared storage, so that several CTAs fit.
 template <typename F>
 cudaError_t allow_smem(F* fn, size_t bytes, int (&done)[64]) {
   int dev = 0;
@@ -374,6 +504,8 @@ cudaError_t allow_smem(F* fn, size_t bytes, int (&done)[64]) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     done[dev] = 1;
   }
@@ -381,13 +513,13 @@ cudaError_t allow_smem(F* fn, size_t bytes, int (&done)[64]) {
 }
 
 template <typename F>
-cudaError_t launch_tiles(F* fn, RParams p, int cols, int lanes, int slots, size_t smem, cudaStream_t stream) {
-  const int tiles = (p.d_out + cols - 1) / cols;
+cudaError_t launch_tiles(F* fn, RParams p, int halves, int slots, size_t smem, cudaStream_t stream) {
+  const int tiles = (p.d_out + 128 * halves - 1) / (128 * halves);
   const int n_blocks = p.d_in / mx4::kBlock;
-  int S = pick_cluster(tiles, n_blocks, lanes, slots);
+  int S = pick_splits(tiles, n_blocks, kRWarps / halves, slots);
   if (p.idx != nullptr) {  // the split's coefficients are staged in shared memory
-    while (((n_blocks + S - 1) / S) * 32 > kMaxSplitRows) S *= 2;
-    smem = std::max(smem, (size_t)((n_blocks + S - 1) / S) * 32 * 4);
+    while (((n_blocks + S - 1) / S) * 32 > kMaxSplitRows) ++S;
+    smem += (size_t)((n_blocks + S - 1) / S) * 32 * 4;
   }
   p.blocks_per_split = (n_blocks + S - 1) / S;
   cudaLaunchConfig_t cfg = {};
@@ -395,16 +527,39 @@ cudaError_t launch_tiles(F* fn, RParams p, int cols, int lanes, int slots, size_
   cfg.blockDim = dim3(kRThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = S;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <bool kList, int kM, int kHalves>
+cudaError_t launch_few(const RParams& p, cudaStream_t stream) {
+  constexpr size_t kBytes = FewSmem<kM>::kBytes;
+  static int done[64] = {0};
+  auto* fn = mx4_rows_few_kernel<kList, kM, kHalves>;
+  const cudaError_t e = allow_smem(fn, kBytes + (kList ? (size_t)kMaxSplitRows * 4 : 0), done);
+  if (e != cudaSuccess) return e;
+  return launch_tiles(fn, p, kHalves, kFewCtas * 148, kBytes, stream);
+}
+
+// 256 columns per CTA where that still gives every SM its CTAs.
+template <bool kList, int kM>
+cudaError_t launch_few(const RParams& p, cudaStream_t stream) {
+  const bool wide = (p.d_out + 255) / 256 * kMaxSplits >= kFewCtas * 148;
+  return wide ? launch_few<kList, kM, 2>(p, stream) : launch_few<kList, kM, 1>(p, stream);
+}
+
+template <int NT>
+cudaError_t launch_many(const RParams& p, cudaStream_t stream) {
+  constexpr size_t kBytes = sizeof(ManyTile<NT>) * kRing * kRWarps;
+  static_assert((size_t)(kRWarps / 2) * 4 * NT * 256 * 4 <= kBytes, "the sums reuse the rings");
+  static int done[64] = {0};
+  cudaError_t e = allow_smem(mx4_rows_many_kernel<NT>, kBytes, done);
+  if (e != cudaSuccess) return e;
+  return launch_tiles(mx4_rows_many_kernel<NT>, p, 2, kManyCtas * 148, kBytes, stream);
 }
 
 // Token groups of four an operand is laid out for (1 to 4 tokens use none).
@@ -424,10 +579,18 @@ mx4::Operand operand_at(void* buf, int M, int d_in) {
 
 bool mx4_rows_take_operand(int M) { return M > 4; }
 
-size_t mx4_rows_buffer_bytes(int M, int d_in) {
-  if (!mx4_rows_take_operand(M)) return (size_t)M * d_in * 4;
+namespace {
+// Bytes of the coefficients at the start of the buffer; the splits' partial
+// sums follow.
+size_t coef_bytes(int M, int d_in) {
   const size_t blocks = (size_t)d_in / mx4::kBlock;
-  return blocks * groups_of(M) * (512 + 4 * 4 + 4 * 4);
+  const size_t n = mx4_rows_take_operand(M) ? blocks * groups_of(M) * (512 + 4 * 4 + 4 * 4) : (size_t)M * d_in * 4;
+  return (n + 255) / 256 * 256;
+}
+}  // namespace
+
+size_t mx4_rows_buffer_bytes(int M, int d_in, int d_out) {
+  return coef_bytes(M, d_in) + (size_t)kMaxSplits * M * ((d_out + 255) / 256 * 256) * 4;
 }
 
 mx4::Operand mx4_rows_operand(void* buf, int M, int d_in) {
@@ -454,44 +617,30 @@ cudaError_t launch_mx4_coef(const int32_t* idx, const float* val, int M, int K, 
                             mx4_rows_operand(buf, M, d_in), dev_status);
 }
 
-cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, const void* buf, int M, const void* codes,
-                            const void* scales, int d_in, int d_out, float* y, int* dev_status,
+cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, void* buf, unsigned* tickets, int M,
+                            const void* codes, const void* scales, int d_in, int d_out, float* y, int* dev_status,
                             cudaStream_t stream) {
   RParams p{};
   p.codes = static_cast<const uint8_t*>(codes);
   p.scales = static_cast<const uint8_t*>(scales);
   p.y = y;
+  p.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(buf) + coef_bytes(M, d_in));
+  p.tickets = tickets;
   p.M = M;
   p.K = K;
   p.d_in = d_in;
   p.d_out = d_out;
   p.dev_status = dev_status;
-  constexpr size_t kFewSmem = (size_t)kRWarps * 4 * 128 * 4;
-  if (idx != nullptr) {
-    if (M != 1) return cudaErrorInvalidValue;
+  if (!mx4_rows_take_operand(M)) {
+    if (idx != nullptr && M != 1) return cudaErrorInvalidValue;
     p.idx = idx;
     p.val = val;
-    static int done[64] = {0};
-    cudaError_t e = allow_smem(mx4_rows_few_kernel<true>, (size_t)kMaxSplitRows * 4, done);
-    if (e != cudaSuccess) return e;
-    return launch_tiles(mx4_rows_few_kernel<true>, p, 128, kRWarps, 2 * 148, kFewSmem, stream);
-  }
-  if (!mx4_rows_take_operand(M)) {
     p.coef = static_cast<const float*>(buf);
-    return launch_tiles(mx4_rows_few_kernel<false>, p, 128, kRWarps, 2 * 148, kFewSmem, stream);
+    if (idx != nullptr) return launch_few<true, 1>(p, stream);
+    return M == 1 ? launch_few<false, 1>(p, stream) : launch_few<false, 4>(p, stream);
   }
-  p.op = operand_at(const_cast<void*>(buf), M, d_in);
-  constexpr size_t kManySmem = (size_t)(kRWarps / 2) * 4 * 256 * 4;  // per token group of four
-  if (M <= 8) {
-    static int done[64] = {0};
-    cudaError_t e = allow_smem(mx4_rows_many_kernel<2>, 2 * kManySmem, done);
-    if (e != cudaSuccess) return e;
-    return launch_tiles(mx4_rows_many_kernel<2>, p, 256, kRWarps / 2, 2 * 148, 2 * kManySmem, stream);
-  }
-  static int done[64] = {0};
-  cudaError_t e = allow_smem(mx4_rows_many_kernel<4>, 4 * kManySmem, done);
-  if (e != cudaSuccess) return e;
-  return launch_tiles(mx4_rows_many_kernel<4>, p, 256, kRWarps / 2, 148, 4 * kManySmem, stream);
+  p.op = operand_at(buf, M, d_in);
+  return M <= 8 ? launch_many<2>(p, stream) : launch_many<4>(p, stream);
 }
 
 }  // namespace larosa
