@@ -293,4 +293,10 @@ cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, void* b
                             const void* codes, const void* scales, int d_in, int d_out, float* y, int* dev_status,
                             cudaStream_t stream);
 
+// Product of two MX4 matrices with blocks along d_in: y [M x d_out] =
+// x [M x d_in] . W^T, W [d_out x d_in] (mx4_linear.cu, tcgen05).
+cudaError_t launch_mx4_linear(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                              int M, int d_in, int d_out, void* y, bool out_bf16, int* dev_status,
+                              cudaStream_t stream);
+
 }  // namespace larosa

@@ -55,6 +55,7 @@ _SIGNATURES = {
     "larosa_sparse_linear_noalloc_bytes": ([_i, _i, _i, _i, _i], _sz),
     "larosa_mx4_quantize": ([_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp], _i),
     "larosa_mx4_dequantize": ([_vp, _vp, _i, _i, _i, _i, _vp, _vp], _i),
+    "larosa_mx4_linear": ([_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp], _i),
     "larosa_mx4_sparse_linear": ([_vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
     "larosa_mx4_topk_linear": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
     "larosa_workspace_sync_offset": ([_i, _i, _i, _i, _c.POINTER(_sz)], _i),
@@ -86,6 +87,7 @@ LAROSA_MAX_SPLIT_K = 8
 LAROSA_MAX_M = 16
 LAROSA_MAX_D = 32768
 LAROSA_MX4_BLOCK = 32
+LAROSA_MX4_MAX_M = 1048576
 LAROSA_NOALLOC_SCRATCH_BYTES = 2 << 20
 
 
@@ -659,6 +661,26 @@ def larosa_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, axis: int =
     _call(_lib.larosa_mx4_dequantize, "larosa_mx4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(),
           rows, cols, axis, _dtype_code(out), out.data_ptr())
     return out
+
+
+def larosa_mx4_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, Wt_codes: torch.Tensor,
+                      Wt_scales: torch.Tensor, dtype: torch.dtype = torch.float32, y: torch.Tensor | None = None,
+                      dev_status: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x . W of two 4-bit matrices, [M, d_out] in `dtype`: x [M, d_in] and the
+    weight in torch.nn.Linear layout [d_out, d_in], both of larosa_mx4_quantize
+    with axis 1."""
+    M, d_in = _mx4_pair(x_codes, x_scales, 1, "x_")
+    d_out, d_w = _mx4_pair(Wt_codes, Wt_scales, 1, "Wt_")
+    dev = Wt_codes.device
+    if d_w != d_in or x_codes.dim() != 2 or Wt_codes.dim() != 2:
+        raise ValueError("x_codes must be [M, d_in / 2], Wt_codes [d_out, d_in / 2]")
+    if x_codes.device != dev:
+        raise ValueError(f"x_codes is on {x_codes.device}, the other tensors are on {dev}")
+    y = _out(y, "y", (M, d_out), dtype if y is None else y.dtype, dev)
+    _call(_lib.larosa_mx4_linear, "larosa_mx4_linear", dev, x_codes.data_ptr(), x_scales.data_ptr(),
+          Wt_codes.data_ptr(), Wt_scales.data_ptr(), M, d_in, d_out, y.data_ptr(), _dtype_code(y),
+          _status_word(dev_status, dev))
+    return y
 
 
 def larosa_mx4_sparse_linear(idx: torch.Tensor, val: torch.Tensor, W_codes: torch.Tensor, W_scales: torch.Tensor,

@@ -79,6 +79,7 @@ typedef struct CUstream_st *larosa_stream_t;
 #define LAROSA_MAX_M 16
 #define LAROSA_MAX_D 32768
 #define LAROSA_MX4_BLOCK 32 /* values that share a scale in the 4-bit format */
+#define LAROSA_MX4_MAX_M 1048576 /* tokens of larosa_mx4_linear */
 
 /* Return codes. */
 typedef enum {
@@ -431,6 +432,21 @@ int larosa_mx4_quantize(const void *src, int rows, int cols, int axis,
 int larosa_mx4_dequantize(const void *codes, const void *scales, int rows,
                           int cols, int axis, int dtype, void *dst,
                           larosa_stream_t stream);
+
+/*
+ * Product of 4-bit activations and a 4-bit weight, one token to a prompt:
+ *   y[m][j] = sum_i x[m][i] * Wt[j][i],
+ * x [M x d_in] and Wt [d_out x d_in] (torch.nn.Linear layout, as for
+ * larosa_dense_linear), both held with axis 1.  On the tensor cores' 4-bit
+ * rate; products exact, fp32 accumulation, y: [M x d_out] of `dtype` (bf16:
+ * rounded once, to nearest even).  1 <= M <= LAROSA_MX4_MAX_M, d_in a multiple
+ * of 32, d_out any; every pointer 16-byte aligned.  Uses no workspace;
+ * results repeat bit for bit.
+ */
+int larosa_mx4_linear(const void *x_codes, const void *x_scales,
+                      const void *Wt_codes, const void *Wt_scales, int M,
+                      int d_in, int d_out, void *y, int dtype, int *dev_status,
+                      larosa_stream_t stream);
 
 /*
  * larosa_sparse_linear with a 4-bit weight:

@@ -54,6 +54,21 @@ def test_sparse_and_topk_linear(lib):
     assert t(FAKE, FAKE, FAKE, 1, 64, 72, 4, FAKE, FAKE, z, None, None) == 3
 
 
+def test_linear(lib):
+    f = lib.larosa_mx4_linear
+    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, FAKE, 5, None, None) == 4
+    assert f(FAKE, None, FAKE, FAKE, 4, 64, 64, FAKE, F32, None, None) == 1
+    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, None, F32, None, None) == 1
+    assert f(FAKE, FAKE, FAKE, FAKE, 0, 64, 64, FAKE, F32, None, None) == 2
+    assert f(FAKE, FAKE, FAKE, FAKE, 1 << 21, 64, 64, FAKE, F32, None, None) == 2
+    assert f(FAKE, FAKE, FAKE, FAKE, 4, 65536, 64, FAKE, F32, None, None) == 2
+    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 0, FAKE, F32, None, None) == 2
+    assert f(FAKE, FAKE, FAKE, FAKE, 4, 72, 64, FAKE, F32, None, None) == 3
+    assert f(MISALIGNED, FAKE, FAKE, FAKE, 4, 64, 64, FAKE, F32, None, None) == 3
+    assert f(FAKE, FAKE, FAKE, MISALIGNED, 4, 64, 64, FAKE, F32, None, None) == 3
+    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, MISALIGNED, F32, None, None) == 3
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     import activation_sparsity_b200 as L
     x = torch.zeros(4, 64)
