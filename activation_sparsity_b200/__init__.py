@@ -24,7 +24,8 @@ _EXPORTS = (
     "larosa_sparse_lowrank_linear", "larosa_lowrank_workspace_bytes", "larosa_sparse_linear_noalloc_bytes",
     "larosa_mx4_quantize", "larosa_mx4_dequantize", "larosa_mx4_linear",
     "larosa_mx4_sparse_linear", "larosa_mx4_topk_linear",
-    "LAROSA_MX4_BLOCK", "LAROSA_MX4_MAX_M",
+    "larosa_moe_layer", "larosa_moe_workspace_bytes",
+    "LAROSA_MX4_BLOCK", "LAROSA_MX4_MAX_M", "LAROSA_MOE_MAX_E", "LAROSA_MOE_MAX_K",
     "larosa_workspace_sync_offset", "larosa_set_wait_limit_ns", "larosa_set_debug", "larosa_set_split_k",
     "LAROSA_OK", "LAROSA_ERR_NONFINITE", "LAROSA_ERR_TIMEOUT", "LAROSA_ERR_INDEX", "LAROSA_ERR_LIST",
     "LAROSA_DEV_NONFINITE", "LAROSA_DEV_TIMEOUT", "LAROSA_DEV_INDEX", "LAROSA_DEV_LIST", "LAROSA_MAX_SPLIT_K",

@@ -25,6 +25,13 @@
 //                              factor products (bf16: coefficient rows from
 //                              lowrank.cu and tcgen05; else the dropped part and
 //                              row-streaming GEMVs), y += y_r
+//   4-bit format               quantise / dequantise (mx4.cu); product of two
+//                              4-bit matrices mx4_linear_kernel (mx4_linear.cu,
+//                              tcgen05); sparse linear with a 4-bit weight:
+//                              coefficients (topk.cu or mx4_coef_kernel, one
+//                              token's list by the product itself), then the
+//                              row kernels of mx4_rows.cu
+//   expert layer               moe_kernel (moe.cu): one cooperative launch
 //   debug checks               check_lists_kernel (debug.cu) around the calls
 //                              that take or write kept lists, when enabled
 #include <stdio.h>
@@ -1101,6 +1108,58 @@ int larosa_mx4_topk_linear(const float* x_rot, const void* W_codes, const void* 
                               W_scales, d_in, d_out, y, dev_status, s);
   if (e != cudaSuccess) return cuda_fail(e, "4-bit sparse linear kernel");
   return check_workspace_lists(M, d_in, d_out, K, ws, dev_status, stream);
+}
+
+static int check_moe_sizes(int M, int d, int f, int E, int k) {
+  if (M < 1 || M > LAROSA_MAX_M || d < 1 || d > LAROSA_MAX_D || f < 1 || f > LAROSA_MAX_D) return LAROSA_ERR_SHAPE;
+  if (E < 1 || E > LAROSA_MOE_MAX_E || k < 1 || k > E || k > LAROSA_MOE_MAX_K) return LAROSA_ERR_SHAPE;
+  return LAROSA_OK;
+}
+
+size_t larosa_moe_workspace_bytes(int M, int d, int f, int E, int k) {
+  if (check_moe_sizes(M, d, f, E, k) != LAROSA_OK) return 0;
+  return align_up(kHeaderEnd, 256) + larosa::moe_buffer_bytes(M, d, f, E, k);
+}
+
+int larosa_moe_layer(const void* x, const void* Wr, const void* W_gu, const void* S_gu, const void* W_d,
+                     const void* S_d, int M, int d, int f, int E, int k, int renormalize, float* y, int32_t* idx,
+                     float* gate, void* ws, size_t ws_bytes, int* dev_status, int dtype, larosa_stream_t stream) {
+  if (!valid_dtype(dtype)) return LAROSA_ERR_UNSUPPORTED_DTYPE;
+  if (x == nullptr || Wr == nullptr || W_gu == nullptr || W_d == nullptr || y == nullptr ||
+      (S_gu == nullptr) != (S_d == nullptr) || (renormalize != 0 && renormalize != 1))
+    return LAROSA_ERR_INVALID_ARG;
+  const int st = check_moe_sizes(M, d, f, E, k);
+  if (st != LAROSA_OK) return st;
+  const bool mx4 = S_gu != nullptr;
+  const int unit = mx4 ? LAROSA_MX4_BLOCK : 8;
+  if (d % unit != 0 || f % unit != 0 || !aligned16(x) || !aligned16(Wr) || !aligned16(W_gu) || !aligned16(S_gu) ||
+      !aligned16(W_d) || !aligned16(S_d) || !aligned16(y))
+    return LAROSA_ERR_ALIGN;
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < larosa_moe_workspace_bytes(M, d, f, E, k))
+    return LAROSA_ERR_WORKSPACE;
+  larosa::MoeArgs a;
+  a.x = x;
+  a.Wr = Wr;
+  a.W_gu = W_gu;
+  a.S_gu = S_gu;
+  a.W_d = W_d;
+  a.S_d = S_d;
+  a.M = M;
+  a.d = d;
+  a.f = f;
+  a.E = E;
+  a.k = k;
+  a.renormalize = renormalize == 1;
+  a.x_elem = elem_of(dtype);
+  a.format = mx4 ? larosa::MoeFormat::MX4 : dtype == LAROSA_BF16 ? larosa::MoeFormat::BF16 : larosa::MoeFormat::F32;
+  a.y = y;
+  a.idx = idx;
+  a.gate = gate;
+  a.sync = reinterpret_cast<unsigned*>(at(ws, kOffTickets));
+  a.buf = at(ws, align_up(kHeaderEnd, 256));
+  a.dev_status = dev_status;
+  const cudaError_t e = larosa::launch_moe(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LAROSA_OK : cuda_fail(e, "expert layer kernel");
 }
 
 int larosa_check(const int* dev_status, larosa_stream_t stream, int* flags_out) {

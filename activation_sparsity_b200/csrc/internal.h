@@ -299,4 +299,30 @@ cudaError_t launch_mx4_linear(const void* x_codes, const void* x_scales, const v
                               int M, int d_in, int d_out, void* y, bool out_bf16, int* dev_status,
                               cudaStream_t stream);
 
+// A mixture-of-experts layer for 1 to 16 tokens in one cooperative launch
+// (moe.cu).  W_gu [E][d][2 f], W_d [E][f][d] in `format` (MX4: codes, with
+// scales S_gu, S_d); x and Wr of x_elem.  `sync`: the workspace's zero-filled
+// header words, `buf`: moe_buffer_bytes of scratch.
+enum class MoeFormat { BF16, F32, MX4 };
+struct MoeArgs {
+  const void* x = nullptr;
+  const void* Wr = nullptr;
+  const void* W_gu = nullptr;
+  const void* S_gu = nullptr;
+  const void* W_d = nullptr;
+  const void* S_d = nullptr;
+  int M = 0, d = 0, f = 0, E = 0, k = 0;
+  bool renormalize = true;
+  Elem x_elem = Elem::BF16;
+  MoeFormat format = MoeFormat::BF16;
+  float* y = nullptr;
+  int32_t* idx = nullptr;
+  float* gate = nullptr;
+  unsigned* sync = nullptr;
+  void* buf = nullptr;
+  int* dev_status = nullptr;
+};
+size_t moe_buffer_bytes(int M, int d, int f, int E, int k);
+cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream);
+
 }  // namespace larosa

@@ -1,0 +1,950 @@
+// A mixture-of-experts layer for 1 to 16 tokens in one kernel (sm_100a):
+//
+//   l[m][e]  = sum_i x[m][i] Wr[e][i]                       router scores
+//   S_m      = the k experts of largest l[m] (ties: the lower index)
+//   p[m][s]  = softmax over S_m (renormalised), or over every expert
+//   h        = silu(x W_gate[e]) * (x W_up[e]),  silu(v) = v / (1 + exp(-v))
+//   y[m]     = sum_s p[m][s] (h[m][s] W_down[e_s])
+//
+// Experts are row-major like every weight of the library: W_gu [E][d][2 f]
+// (gate | up along the columns) and W_d [E][f][d], in bf16, fp32 or MX4 with
+// blocks down the rows.
+//
+// Few tokens make it a stream of the chosen experts' weights, bound by HBM
+// (bf16: one product per 2 bytes and token), in three phases that depend on
+// one another: scores, then gate|up, then down.  As three launches the two
+// boundaries cost a drain, a launch and a ramp each, more than the whole
+// stream of a small layer; here one cooperative grid passes two grid-wide
+// barriers, and a CTA asks for its first down rows to be brought into L2
+// before it waits at the second.
+//
+//   scores   a warp per expert and four tokens, summed in fp64: selection is
+//            a comparison, so scores that differ by less than fp32 rounding
+//            must not swap.  (Products of two fp32 values are exact in fp64.)
+//   routing  every CTA makes the same selection and the same work list from
+//            the scores.  A group is an expert and up to eight of its tokens.
+//   products a unit is a group, a tile of columns (gate and up halves side by
+//            side) and a split of the rows.  The CTA's eight warps take rows
+//            in turn, their sums are added in warp order in shared memory,
+//            the splits' (and for down also the experts') sums go through the
+//            workspace and the last unit of a tile to arrive adds them in a
+//            fixed order: results repeat bit for bit.  The number of splits
+//            follows from the number of groups, so that there are units for
+//            all CTAs.
+//
+// The products run on mma.sync.m16n8k16 with fp32 accumulators: eight tokens
+// of fp32 FMAs per 2-byte weight would be the limit instead of HBM.  A lane
+// loads 16 bytes (eight columns) of four rows of a 16-row step, so that every
+// weight row is read in 128-byte segments, and two byte permutations make
+// the A operand's pairs along the reduction; the tokens are the eight columns
+// of B.  The bf16 input is its own operand; h, an fp32 value, enters as three
+// bf16 pieces (24 significant bits) into the same accumulator.  4-bit experts
+// use the block products of mx4_mma.cuh, with x and h as two f16 pieces per
+// block of 32.  fp32 experts use fp32 FMAs.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx4_mma.cuh"
+
+namespace larosa {
+namespace {
+
+constexpr int kT = 256;
+constexpr int kWarps = kT / 32;
+constexpr int kGroup = 8;      // tokens of a group
+constexpr int kMaxE = 512;     // LAROSA_MOE_MAX_E
+constexpr int kMaxK = 16;      // LAROSA_MOE_MAX_K
+constexpr int kMaxPairs = 16 * kMaxK;
+constexpr int kMaxSplits = 8;
+constexpr int kCtasPerSm = 2;
+
+enum class Fmt { BF16, F32, MX4 };
+
+// Words of the workspace's zero-filled header: arrivals at the two barriers
+// and at the end, then the tickets of the two product phases.
+constexpr int kSyncA = 0, kSyncB = 1, kSyncEnd = 2;
+constexpr int kTickets1 = 16, kTickets2 = 1024;
+
+struct MParams {
+  const void* x;
+  const void* wr;
+  const uint8_t* gu;
+  const uint8_t* gus;
+  const uint8_t* dn;
+  const uint8_t* dns;
+  float* y;
+  int32_t* idx;  // may be null
+  float* gate;   // may be null
+  unsigned* sync;
+  double* logits;        // [M][E]
+  unsigned char* xop;    // MX4: x's pieces [M][2][d] f16, then scales [M][d / 32]
+  unsigned char* hop;    // h: bf16 pieces [pairs][3][f], fp32 [pairs][f], or as xop
+  float* part1;          // [splits][pairs][2 f]
+  float* part2;          // [splits][pairs][d]
+  int M, d, f, E, k;
+  int cap1, cap2;        // most splits the workspace holds
+  int renormalize;
+  int x_f32;             // MX4 experts: x and Wr are fp32
+  int* dev_status;
+  unsigned long long wait_ns;
+};
+
+// The routing of a call, the same in every CTA.
+struct Routing {
+  double top[16][kMaxK];
+  float gate[kMaxPairs];
+  int expert[kMaxPairs];
+  int cnt[kMaxE];
+  int base[kMaxE];
+  short g_expert[kMaxPairs];
+  short g_n[kMaxPairs];
+  short g_pair[kMaxPairs][kGroup];
+  int groups;
+  int ok;
+  unsigned order;
+};
+
+// ---------------------------------------------------------------- grid-wide barrier
+
+// Every CTA of the (co-resident) grid arrives at *word, which counts up from
+// zero; false once the wait limit has passed.
+__device__ __forceinline__ bool grid_barrier(unsigned* word, Routing* r, const MParams& p) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    atomic_add_release_gpu(word, 1u);
+    const unsigned n = gridDim.x;
+    unsigned seen;
+    bool ok = true;
+    unsigned long long t0 = 0;
+    for (unsigned it = 0;; ++it) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(word) : "memory");
+      if (seen == n) break;  // it stays there until every CTA has passed
+      if ((it & 63u) == 63u) {
+        const unsigned long long now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > p.wait_ns) {
+          ok = false;
+          break;
+        }
+      }
+    }
+    r->ok = ok;
+    if (!ok) report(p.dev_status, LAROSA_DEV_TIMEOUT);
+  }
+  __syncthreads();
+  return r->ok != 0;
+}
+
+// ---------------------------------------------------------------- scores
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// Warp tasks (expert, four tokens), dealt over the grid so that few tasks
+// land on many SMs.
+template <typename T>
+__device__ void scores(const MParams& p) {
+  const int lane = threadIdx.x & 31;
+  const int tg = (p.M + 3) / 4;
+  const T* x = static_cast<const T*>(p.x);
+  const T* wr = static_cast<const T*>(p.wr);
+  for (int task = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; task < p.E * tg; task += kWarps * gridDim.x) {
+    const int e = task / tg, m0 = task % tg * 4;
+    const T* w = wr + (size_t)e * p.d;
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 2
+    for (int i = lane * 8; i < p.d; i += 256) {
+      float wv[8];
+      load8<T>(w + i, wv);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (m0 + m < p.M) {
+          float xv[8];
+          load8<T>(x + (size_t)(m0 + m) * p.d + i, xv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[m] = fma((double)wv[j], (double)xv[j], acc[m]);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
+      if (lane == 0 && m0 + m < p.M) __stcg(p.logits + (size_t)(m0 + m) * p.E + e, acc[m]);
+    }
+  }
+}
+
+// v of row `lane` of block `b` of token (or pair) m as MX4 pieces: op holds
+// [count][2][n] f16, then [count][n / 32] scales.
+__device__ __forceinline__ void put_pieces(unsigned char* op, int count, int n, int m, int b, float v, int lane) {
+  const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
+  float up, down;
+  mx4::piece_scale(top, &up, &down);
+  __half p0, p1;
+  mx4::split_pieces(v * up, &p0, &p1);
+  __half* row = reinterpret_cast<__half*>(op) + (size_t)m * 2 * n + b * 32 + lane;
+  row[0] = p0;
+  row[n] = p1;
+  if (lane == 0) reinterpret_cast<float*>(op + (size_t)count * 4 * n)[(size_t)m * (n / 32) + b] = down;
+}
+
+// ---------------------------------------------------------------- routing
+
+// A score's place in the order: larger scores have larger keys, a NaN the
+// smallest of all (1); 0 is left for "taken".
+__device__ __forceinline__ unsigned long long score_key(double v) {
+  if (v != v) return 1ull;
+  v += 0.0;  // -0 counts as +0
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v);
+  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+
+// Selection and softmax of token m by one warp.
+__device__ void route_token(const MParams& p, Routing* r, int m) {
+  const int lane = threadIdx.x & 31;
+  const double* l = p.logits + (size_t)m * p.E;
+  unsigned long long key[kMaxE / 32];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kMaxE / 32; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = 0ull;
+    if (e < p.E) {
+      const double v = __ldcg(l + e);
+      key[i] = score_key(v);
+      bad |= !isfinite(v);
+    }
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) report(p.dev_status, LAROSA_DEV_NONFINITE);
+  for (int s = 0; s < p.k; ++s) {
+    unsigned long long best = 0ull;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    const unsigned hi = (unsigned)(best >> 32);
+    const unsigned mh = __reduce_max_sync(0xffffffffu, hi);
+    const unsigned ml = __reduce_max_sync(0xffffffffu, hi == mh ? (unsigned)best : 0u);
+    const bool mine = hi == mh && (unsigned)best == ml;
+    const unsigned e = __reduce_min_sync(0xffffffffu, mine ? (unsigned)(lane + 32 * at) : 0xffffffffu);
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; ++i)
+      if ((unsigned)(lane + 32 * i) == e) key[i] = 0ull;
+    if (lane == 0) {
+      r->expert[m * p.k + s] = (int)e;
+      r->top[m][s] = __ldcg(l + e);
+    }
+  }
+  __syncwarp();
+  const double l0 = r->top[m][0];
+  float den = 0.f;
+  if (p.renormalize) {
+    for (int s = 0; s < p.k; ++s) den += expf((float)(r->top[m][s] - l0));
+  } else {
+    for (int e = lane; e < p.E; e += 32) den += expf((float)(__ldcg(l + e) - l0));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  }
+  for (int s = lane; s < p.k; s += 32) {
+    const float g = expf((float)(r->top[m][s] - l0)) / den;
+    r->gate[m * p.k + s] = g;
+    if (blockIdx.x == 0) {
+      if (p.idx != nullptr) p.idx[m * p.k + s] = r->expert[m * p.k + s];
+      if (p.gate != nullptr) p.gate[m * p.k + s] = g;
+    }
+  }
+}
+
+// The groups: experts in ascending order, each one's pairs (token, slot) in
+// ascending order, eight to a group.
+__device__ void build_groups(const MParams& p, Routing* r) {
+  const int tid = threadIdx.x;
+  const int pairs = p.M * p.k;
+  for (int e = tid; e < p.E; e += kT) r->cnt[e] = 0;
+  __syncthreads();
+  for (int q = tid; q < pairs; q += kT) atomicAdd(&r->cnt[r->expert[q]], 1);
+  __syncthreads();
+  if (tid < 32) {
+    int before = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + tid;
+      const int n = e < p.E ? (r->cnt[e] + kGroup - 1) / kGroup : 0;
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (tid >= o) incl += v;
+      }
+      if (e < p.E) r->base[e] = before + incl - n;
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (tid == 0) r->groups = before;
+  }
+  __syncthreads();
+  for (int q = tid; q < pairs; q += kT) {
+    const int e = r->expert[q];
+    int rank = 0;
+    for (int o = 0; o < q; ++o) rank += r->expert[o] == e;
+    const int g = r->base[e] + rank / kGroup;
+    r->g_pair[g][rank % kGroup] = (short)q;
+    if (rank % kGroup == 0) {
+      r->g_expert[g] = (short)e;
+      r->g_n[g] = (short)min(kGroup, r->cnt[e] - rank);
+    }
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------- products
+
+// One unit's operands: rows [k0, k1) of a matrix with `rows` rows and `ld`
+// columns, two column segments at cA and cB with `wA` and `wB` valid columns.
+struct Unit {
+  const uint8_t* W;       // the expert's matrix (MX4: codes)
+  const uint8_t* scales;  // MX4
+  int rows, ld;
+  int cA, cB, wA, wB;
+  int k0, k1;
+  int n;  // tokens
+};
+
+template <Fmt F>
+struct Cfg;
+template <>
+struct Cfg<Fmt::BF16> {
+  static constexpr int kSeg = 64;    // columns of a segment
+  static constexpr int kStep = 16;   // rows a warp takes at a time
+  static constexpr size_t kSmem = (size_t)kWarps * kGroup * 2 * kSeg * 4;
+};
+template <>
+struct Cfg<Fmt::F32> {
+  static constexpr int kSeg = 64;
+  static constexpr int kStep = 32;
+  static constexpr size_t kCoef = (size_t)kWarps * 32 * kGroup * 4;  // a warp's 32 rows of coefficients
+  static constexpr size_t kSmem = (size_t)kWarps * kGroup * 2 * kSeg * 4 + kCoef;
+};
+template <>
+struct Cfg<Fmt::MX4> {
+  static constexpr int kSeg = 128;
+  static constexpr int kStep = 32;
+  static constexpr int kRing = 2;
+  static constexpr size_t kSmem = (size_t)kWarps * kRing * 2 * sizeof(mx4::Tile);
+  static_assert(kSmem >= (size_t)kWarps * kGroup * 2 * kSeg * 4, "the sums reuse the rings");
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+// bf16 weights: sums of this warp's rows to part[warp][token][column].  The
+// operand of the token in column g of B is P rows of `stride` bf16 values at
+// `op` (null: no token).
+template <int P>
+__device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16* op, int stride, float* part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const bool inA = 8 * g < u.wA, inB = 8 * g < u.wB;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const size_t row_bytes = (size_t)u.ld * 2;
+  const uint8_t* base = u.W + (size_t)(4 * t) * row_bytes;
+  const size_t offA = (size_t)(u.cA + 8 * g) * 2, offB = (size_t)(u.cB + 8 * g) * 2;
+  float acc[2][4][4] = {};
+  struct Rows {
+    uint4 w[2][4];
+    uint2 b[P];
+  };
+  auto load = [&](int r0, Rows& s) {
+    const bool in = r0 + 4 * t < u.k1;  // rows and splits are multiples of four
+    const uint8_t* at = base + (size_t)r0 * row_bytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s.w[0][i] = in && inA ? __ldcs(reinterpret_cast<const uint4*>(at + i * row_bytes + offA)) : zero;
+      s.w[1][i] = in && inB ? __ldcs(reinterpret_cast<const uint4*>(at + i * row_bytes + offB)) : zero;
+    }
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+      s.b[q] = in && op != nullptr ? *reinterpret_cast<const uint2*>(op + (size_t)q * stride + r0 + 4 * t)
+                                   : make_uint2(0u, 0u);
+  };
+  auto multiply = [&](const Rows& s) {
+#pragma unroll
+    for (int seg = 0; seg < 2; ++seg)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = q == 0 ? s.w[seg][i].x : q == 1 ? s.w[seg][i].y : q == 2 ? s.w[seg][i].z : s.w[seg][i].w;
+        const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[0], w[1], 0x7632);
+        const uint32_t a2 = __byte_perm(w[2], w[3], 0x5410), a3 = __byte_perm(w[2], w[3], 0x7632);
+#pragma unroll
+        for (int c = 0; c < P; ++c) mma_bf16(acc[seg][q], a0, a1, a2, a3, s.b[c]);
+      }
+  };
+  constexpr int kStride = kWarps * 16;
+  Rows s0, s1;
+  int r = u.k0 + warp * 16;
+  if (r < u.k1) load(r, s0);
+  while (r < u.k1) {
+    if (r + kStride < u.k1) load(r + kStride, s1);
+    multiply(s0);
+    r += kStride;
+    if (r >= u.k1) break;
+    if (r + kStride < u.k1) load(r + kStride, s0);
+    multiply(s1);
+    r += kStride;
+  }
+#pragma unroll
+  for (int seg = 0; seg < 2; ++seg)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float* at = part + ((size_t)warp * kGroup + 2 * t) * 128 + 64 * seg + 8 * g + 2 * q;
+      *reinterpret_cast<float2*>(at) = make_float2(acc[seg][q][0], acc[seg][q][2]);
+      *reinterpret_cast<float2*>(at + 128) = make_float2(acc[seg][q][1], acc[seg][q][3]);
+    }
+}
+
+// fp32 weights: lanes 0-15 hold four columns each of segment A, the others of
+// B; the rows' coefficients of every token lie in the warp's part of `coef`.
+template <int N>
+__device__ __forceinline__ void product_f32(const Unit& u, const float* const (&op)[kGroup], float* coef, float* part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seg = lane >> 4, c = 4 * (lane & 15);
+  const bool in = c < (seg == 0 ? u.wA : u.wB);
+  const float* base = reinterpret_cast<const float*>(u.W) + (seg == 0 ? u.cA : u.cB) + c;
+  float* mine = coef + warp * 32 * kGroup;  // [row][token]
+  float acc[N][4] = {};
+  for (int r0 = u.k0 + warp * 32; r0 < u.k1; r0 += kWarps * 32) {
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+      mine[lane * kGroup + m] = op[m] != nullptr && r0 + lane < u.k1 ? op[m][r0 + lane] : 0.f;
+    __syncwarp();
+    const int n = min(32, u.k1 - r0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 8) {
+      float4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = in && i0 + i < n ? __ldcs(reinterpret_cast<const float4*>(base + (size_t)(r0 + i0 + i) * u.ld))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int m = 0; m < N; ++m) {
+          const float v = mine[(i0 + i) * kGroup + m];
+          acc[m][0] = fmaf(v, w[i].x, acc[m][0]);
+          acc[m][1] = fmaf(v, w[i].y, acc[m][1]);
+          acc[m][2] = fmaf(v, w[i].z, acc[m][2]);
+          acc[m][3] = fmaf(v, w[i].w, acc[m][3]);
+        }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < N; ++m)
+    *reinterpret_cast<float4*>(part + ((size_t)warp * kGroup + m) * 128 + 64 * seg + c) =
+        make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+}
+
+// MX4 weights: blocks of 32 rows, both segments of a block through the warp's
+// ring of tiles.  op[n], sx[n]: pieces (this lane's column: token 4 n + g / 2,
+// piece g % 2) and block scales of token 4 n + t (null: no token).
+template <int NT>
+__device__ __forceinline__ void product_mx4(const Unit& u, const __half* const (&op)[NT], const float* const (&sx)[NT],
+                                            unsigned char* smem) {
+  constexpr int kRing = Cfg<Fmt::MX4>::kRing;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  mx4::Tile(*ring)[2] = reinterpret_cast<mx4::Tile(*)[2]>(smem) + warp * kRing;
+  const uint32_t row_bytes = (uint32_t)u.ld / 2;
+  float acc[2][NT][8][2] = {};
+  const int b0 = u.k0 / 32, b1 = u.k1 / 32;
+  auto copy = [&](int b, int s) {
+    if (b < b1) {
+#pragma unroll
+      for (int seg = 0; seg < 2; ++seg) {
+        const int c0 = seg == 0 ? u.cA : u.cB, w = seg == 0 ? u.wA : u.wB;
+        if (w > 0) {
+          mx4::Tile& tile = ring[s][seg];
+          // columns past the segment name its last ones
+          const uint32_t chunk = (uint32_t)c0 / 2 + min(16u * (lane & 3), (uint32_t)w / 2 - 16u);
+          const uint8_t* from = u.W + (size_t)b * 32 * row_bytes + chunk;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int pos = 8 * j + (lane >> 2);
+            const uint32_t row = (pos & 16) + (pos & 3) * 4 + ((pos >> 2) & 3);
+            mx4::copy16_l2(&tile.row[pos][16 * (lane & 3)], from + row * row_bytes);
+          }
+          if (lane < 8)
+            mx4::copy16_l2(&tile.scale[16 * lane], u.scales + (size_t)b * u.ld + c0 + min(16 * lane, w - 16));
+        }
+      }
+    }
+    mx4::copies_commit();
+  };
+  int b = b0 + warp;
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) copy(b + s * kWarps, s);
+  for (int it = 0; b < b1; b += kWarps, ++it) {
+    uint2 bop[2][NT];
+    float s[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int step = 0; step < 2; ++step)
+        bop[step][n] = op[n] != nullptr ? *reinterpret_cast<const uint2*>(op[n] + b * 32 + 16 * step + 4 * t)
+                                        : make_uint2(0u, 0u);
+      s[n] = sx[n] != nullptr ? sx[n][b] : 0.f;
+    }
+    __syncwarp();  // every lane has read the tiles that are filled next
+    copy(b + (kRing - 1) * kWarps, (it + kRing - 1) % kRing);
+    mx4::copies_wait<kRing - 1>();
+    __syncwarp();  // the other lanes' copies too
+#pragma unroll
+    for (int seg = 0; seg < 2; ++seg) {
+      if ((seg == 0 ? u.wA : u.wB) <= 0) continue;
+      mx4::RowSet rs;
+      rs.read<4, 4>(ring[it % kRing][seg], g, t);
+      mx4::block_product<NT, 4, 4>(rs, bop, s, acc[seg]);
+    }
+  }
+  mx4::copies_wait<0>();
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(smem);  // [warp][token][256]
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int seg = 0; seg < 2; ++seg)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<float2*>(part + ((size_t)warp * kGroup + 4 * n + t) * 256 + 128 * seg + 16 * g + 2 * q) =
+            make_float2(acc[seg][n][q][0], acc[seg][n][q][1]);
+}
+
+// The unit's sums over the CTA's warps end up in part[warp 0][token][column].
+// op of a pair: x's (phase 1: token q / k) or h's (phase 2: pair q) operand.
+template <Fmt F, bool kDown>
+__device__ void unit_product(const MParams& p, const Routing* r, int group, const Unit& u, unsigned char* smem) {
+  constexpr int kCols = 2 * Cfg<F>::kSeg;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rows = u.rows;
+  float* part = reinterpret_cast<float*>(smem);
+  auto operand = [&](int pos) -> int {  // row of the operand of the group's pos-th pair, -1: none
+    if (pos >= u.n) return -1;
+    const int q = r->g_pair[group][pos];
+    return kDown ? q : q / p.k;
+  };
+  __syncthreads();  // the sums of the unit before are used up
+  if constexpr (F == Fmt::BF16) {
+    const int o = operand(g);
+    if constexpr (kDown)
+      product_bf16<3>(u, o < 0 ? nullptr : reinterpret_cast<const __nv_bfloat16*>(p.hop) + (size_t)o * 3 * rows, rows,
+                      part);
+    else
+      product_bf16<1>(u, o < 0 ? nullptr : static_cast<const __nv_bfloat16*>(p.x) + (size_t)o * rows, rows, part);
+  } else if constexpr (F == Fmt::F32) {
+    const float* src = kDown ? reinterpret_cast<const float*>(p.hop) : static_cast<const float*>(p.x);
+    const float* op[kGroup];
+#pragma unroll
+    for (int m = 0; m < kGroup; ++m) {
+      const int o = operand(m);
+      op[m] = o < 0 ? nullptr : src + (size_t)o * rows;
+    }
+    float* coef = part + (size_t)kWarps * kGroup * kCols;
+    if (u.n <= 1)
+      product_f32<1>(u, op, coef, part);
+    else if (u.n <= 2)
+      product_f32<2>(u, op, coef, part);
+    else if (u.n <= 4)
+      product_f32<4>(u, op, coef, part);
+    else
+      product_f32<8>(u, op, coef, part);
+  } else {
+    const unsigned char* src = kDown ? p.hop : p.xop;
+    const __half* pieces = reinterpret_cast<const __half*>(src);
+    const float* scales = reinterpret_cast<const float*>(src + (size_t)(kDown ? p.M * p.k : p.M) * 4 * rows);
+    auto run = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      const __half* op[NT];
+      const float* sx[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int a = operand(4 * n + (g >> 1)), b = operand(4 * n + t);
+        op[n] = a < 0 ? nullptr : pieces + ((size_t)a * 2 + (g & 1)) * rows;
+        sx[n] = b < 0 ? nullptr : scales + (size_t)b * (rows / 32);
+      }
+      product_mx4<NT>(u, op, sx, smem);
+    };
+    if (u.n <= 4)
+      run(std::integral_constant<int, 1>{});
+    else
+      run(std::integral_constant<int, 2>{});
+  }
+  __syncthreads();
+  for (int e = tid; e < u.n * kCols; e += kT) {
+    float s = part[e];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) s += part[(size_t)w * kGroup * kCols + e];
+    part[e] = s;  // this thread's own element
+  }
+  __syncthreads();
+}
+
+// h of pair q, column j: stored as the operand of the down product.  Lanes of
+// a warp hold neighbouring columns.
+template <Fmt F>
+__device__ __forceinline__ void put_h(const MParams& p, int q, int j, float g, float u, int lane) {
+  const float h = g / (1.f + expf(-g)) * u;
+  if constexpr (F == Fmt::BF16) {
+    __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(p.hop) + (size_t)q * 3 * p.f + j;
+    const __nv_bfloat16 a = __float2bfloat16_rn(h);
+    const float r1 = h - __bfloat162float(a);
+    const __nv_bfloat16 b = __float2bfloat16_rn(r1);
+    at[0] = a;
+    at[p.f] = b;
+    at[2 * p.f] = __float2bfloat16_rn(r1 - __bfloat162float(b));
+  } else if constexpr (F == Fmt::F32) {
+    reinterpret_cast<float*>(p.hop)[(size_t)q * p.f + j] = h;
+  } else {
+    put_pieces(p.hop, p.M * p.k, p.f, q, j / 32, h, lane);
+  }
+}
+
+// True in every thread of the CTA that arrives last of `count` at a ticket,
+// which is zero again then.
+__device__ __forceinline__ bool last_to_arrive(unsigned* ticket, unsigned count, Routing* r) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned order = atomic_add_acq_rel_gpu(ticket, 1u);
+    r->order = order;
+    if (order == count - 1u) *ticket = 0u;
+  }
+  __syncthreads();
+  return r->order == count - 1u;
+}
+
+__device__ __forceinline__ int splits_for(int units, int steps, int cap) {
+  return max(1, min(min(cap, (int)gridDim.x / max(units, 1)), steps));
+}
+
+// Rows [k0, k1) of split s of S: whole steps.
+__device__ __forceinline__ void split_rows(int rows, int step, int S, int s, int* k0, int* k1) {
+  const int steps = (rows + step - 1) / step;
+  *k0 = (int)((long long)steps * s / S) * step;
+  *k1 = min(rows, (int)((long long)steps * (s + 1) / S) * step);
+}
+
+template <Fmt F>
+__device__ __forceinline__ size_t row_bytes_of(int cols) {
+  return F == Fmt::BF16 ? (size_t)cols * 2 : F == Fmt::F32 ? (size_t)cols * 4 : (size_t)cols / 2;
+}
+
+template <Fmt F>
+__global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Routing r;
+  constexpr int kSeg = Cfg<F>::kSeg, kCols = 2 * kSeg, kStep = Cfg<F>::kStep;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pairs = p.M * p.k;
+
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ------------------------------------------------------------------ scores
+  const bool x_f32 = F == Fmt::F32 || (F == Fmt::MX4 && p.x_f32);
+  if (x_f32)
+    scores<float>(p);
+  else
+    scores<__nv_bfloat16>(p);
+  if constexpr (F == Fmt::MX4) {
+    const int blocks = p.d / 32;
+    for (int i = warp * gridDim.x + blockIdx.x; i < p.M * blocks; i += kWarps * gridDim.x) {
+      const int m = i / blocks, b = i % blocks;
+      const size_t at = (size_t)m * p.d + b * 32 + lane;
+      const float v = x_f32 ? static_cast<const float*>(p.x)[at]
+                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.x)[at]);
+      put_pieces(p.xop, p.M, p.d, m, b, v, lane);
+    }
+  }
+  if (!grid_barrier(p.sync + kSyncA, &r, p)) return;
+
+  // ------------------------------------------------------------------ routing
+  for (int m = warp; m < p.M; m += kWarps) route_token(p, &r, m);
+  __syncthreads();
+  build_groups(p, &r);
+  const int G = r.groups;
+
+  // ------------------------------------------------------------------ gate | up
+  float* part = reinterpret_cast<float*>(smem);
+  {
+    const int tiles = (p.f + kSeg - 1) / kSeg;
+    const int S = splits_for(G * tiles, (p.d + kStep * kWarps - 1) / (kStep * kWarps), p.cap1);
+    const size_t expert_bytes = row_bytes_of<F>(2 * p.f) * p.d;
+    for (int w = blockIdx.x; w < G * tiles * S; w += gridDim.x) {
+      const int group = w % G, split = w / G % S, tile = w / G / S;
+      const int e = r.g_expert[group];
+      Unit u;
+      u.W = p.gu + (size_t)e * expert_bytes;
+      u.scales = F == Fmt::MX4 ? p.gus + (size_t)e * (p.d / 32) * (2 * p.f) : nullptr;
+      u.rows = p.d;
+      u.ld = 2 * p.f;
+      u.cA = tile * kSeg;
+      u.cB = p.f + tile * kSeg;
+      u.wA = u.wB = min(kSeg, p.f - tile * kSeg);
+      u.n = r.g_n[group];
+      split_rows(p.d, kStep, S, split, &u.k0, &u.k1);
+      unit_product<F, false>(p, &r, group, u, smem);
+      if (S == 1) {
+        for (int i = tid; i < u.n * kSeg; i += kT) {
+          const int pos = i / kSeg, j = i % kSeg;
+          if (j < u.wA)
+            put_h<F>(p, r.g_pair[group][pos], u.cA + j, part[pos * kCols + j], part[pos * kCols + kSeg + j], lane);
+        }
+        continue;
+      }
+      for (int i = tid; i < u.n * kCols; i += kT) {
+        const int pos = i / kCols, c = i % kCols, j = c % kSeg;
+        if (j < u.wA)
+          __stcg(p.part1 + ((size_t)split * pairs + r.g_pair[group][pos]) * (2 * p.f) + (c < kSeg ? u.cA : u.cB) + j,
+                 part[i]);
+      }
+      if (!last_to_arrive(p.sync + kTickets1 + tile * G + group, S, &r)) continue;
+      for (int i = tid; i < u.n * kSeg; i += kT) {
+        const int pos = i / kSeg, j = i % kSeg;
+        if (j >= u.wA) continue;
+        const int q = r.g_pair[group][pos];
+        const float* at = p.part1 + (size_t)q * (2 * p.f) + u.cA + j;
+        const size_t step = (size_t)pairs * (2 * p.f);
+        float a[kMaxSplits], b[kMaxSplits];
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s) {
+          a[s] = s < S ? __ldcg(at + s * step) : 0.f;
+          b[s] = s < S ? __ldcg(at + s * step + p.f) : 0.f;
+        }
+        float ga = 0.f, up = 0.f;
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s) {
+          ga += a[s];
+          up += b[s];
+        }
+        put_h<F>(p, q, u.cA + j, ga, up, lane);
+      }
+    }
+  }
+
+  // ------------------------------------------------------------------ down
+  const int tiles = (p.d + kCols - 1) / kCols;
+  const int S = splits_for(G * tiles, (p.f + kStep * kWarps - 1) / (kStep * kWarps), p.cap2);
+  const size_t expert_bytes = row_bytes_of<F>(p.d) * p.f;
+  auto make_unit = [&](int w, int* group, int* split, int* tile) {
+    *group = w % G;
+    *split = w / G % S;
+    *tile = w / G / S;
+    const int e = r.g_expert[*group];
+    Unit u;
+    u.W = p.dn + (size_t)e * expert_bytes;
+    u.scales = F == Fmt::MX4 ? p.dns + (size_t)e * (p.f / 32) * p.d : nullptr;
+    u.rows = p.f;
+    u.ld = p.d;
+    u.cA = *tile * kCols;
+    u.cB = u.cA + kSeg;
+    u.wA = min(kSeg, p.d - u.cA);
+    u.wB = max(0, min(kSeg, p.d - u.cB));
+    u.n = r.g_n[*group];
+    split_rows(p.f, kStep, S, *split, &u.k0, &u.k1);
+    return u;
+  };
+  if ((int)blockIdx.x < G * tiles * S) {
+    // the first unit's rows on their way to L2 while the grid assembles
+    int group, split, tile;
+    const Unit u = make_unit(blockIdx.x, &group, &split, &tile);
+    const size_t row = row_bytes_of<F>(p.d);
+    const size_t c0 = row_bytes_of<F>(u.cA), width = row_bytes_of<F>(u.wA + u.wB);
+    const int lines = (int)((width + 127) / 128);
+    for (int i = tid; i < (u.k1 - u.k0) * lines; i += kT) {
+      const uint8_t* at = u.W + (size_t)(u.k0 + i / lines) * row + c0 + min((size_t)(i % lines) * 128, width - 1);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+  }
+  if (!grid_barrier(p.sync + kSyncB, &r, p)) return;
+  for (int w = blockIdx.x; w < G * tiles * S; w += gridDim.x) {
+    int group, split, tile;
+    const Unit u = make_unit(w, &group, &split, &tile);
+    unit_product<F, true>(p, &r, group, u, smem);
+    for (int i = tid; i < u.n * kCols; i += kT) {
+      const int pos = i / kCols, c = i % kCols;
+      if (u.cA + c < p.d)
+        __stcg(p.part2 + ((size_t)split * pairs + r.g_pair[group][pos]) * p.d + u.cA + c, part[i]);
+    }
+    if (!last_to_arrive(p.sync + kTickets2 + tile, (unsigned)(G * S), &r)) continue;
+    const int width = min(kCols, p.d - u.cA);
+    for (int i = tid; i < p.M * width; i += kT) {
+      const int m = i / width, c = u.cA + i % width;
+      float y = 0.f;
+      for (int s0 = 0; s0 < p.k; ++s0) {
+        const float* at = p.part2 + (size_t)(m * p.k + s0) * p.d + c;
+        float v[kMaxSplits];
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s) v[s] = s < S ? __ldcg(at + (size_t)s * pairs * p.d) : 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s) sum += v[s];
+        y = fmaf(r.gate[m * p.k + s0], sum, y);
+      }
+      p.y[(size_t)m * p.d + c] = y;
+    }
+  }
+
+  // the barriers' words are zero again once every CTA has passed both
+  __syncthreads();
+  if (tid == 0 && atomic_add_acq_rel_gpu(p.sync + kSyncEnd, 1u) == gridDim.x - 1u) {
+    p.sync[kSyncA] = 0u;
+    p.sync[kSyncB] = 0u;
+    p.sync[kSyncEnd] = 0u;
+  }
+}
+
+int seg_of(MoeFormat f) { return f == MoeFormat::MX4 ? 128 : 64; }
+
+// Most splits a phase can use: there are at least k groups (a token's experts
+// differ) and one for every eight pairs.
+int split_cap(int M, int k, int tiles, int grid) {
+  const int groups = std::max(k, (M * k + kGroup - 1) / kGroup);
+  return std::max(1, std::min(kMaxSplits, grid / std::max(1, groups * tiles)));
+}
+
+struct MoePlan {
+  int cap1, cap2;
+  size_t logits, xop, hop, part1, part2, total;
+};
+
+MoePlan make_plan(int M, int d, int f, int E, int k, MoeFormat fmt) {
+  MoePlan pl;
+  const int seg = seg_of(fmt);
+  const int grid = 148 * kCtasPerSm;
+  pl.cap1 = split_cap(M, k, (f + seg - 1) / seg, grid);
+  pl.cap2 = split_cap(M, k, (d + 2 * seg - 1) / (2 * seg), grid);
+  const size_t pairs = (size_t)M * k;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  pl.logits = take((size_t)M * E * 8);
+  pl.xop = take(fmt == MoeFormat::MX4 ? (size_t)M * d * 4 + (size_t)M * (d / 32) * 4 : 0);
+  pl.hop = take(pairs * f * (fmt == MoeFormat::BF16 ? 6 : 4) + pairs * (f / 32 + 1) * 4);
+  pl.part1 = take(pl.cap1 > 1 ? (size_t)pl.cap1 * pairs * 2 * f * 4 : 0);
+  pl.part2 = take((size_t)pl.cap2 * pairs * d * 4);
+  pl.total = off;
+  return pl;
+}
+
+template <Fmt F>
+cudaError_t launch_fmt(const MParams& p, cudaStream_t stream) {
+  static int grids[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (grids[dev] == 0) {
+    int sms = 0, per = 0;
+    e = cudaFuncSetAttribute(moe_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<F>::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(moe_kernel<F>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, moe_kernel<F>, kT, Cfg<F>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (per < 1) return cudaErrorLaunchOutOfResources;
+    // at most the grid that the split caps were made for
+    grids[dev] = std::min(std::min(per, kCtasPerSm) * sms, kCtasPerSm * 148);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grids[dev], 1, 1);
+  cfg.blockDim = dim3(kT, 1, 1);
+  cfg.dynamicSmemBytes = Cfg<F>::kSmem;
+  cfg.stream = stream;
+  // every CTA must be resident at once: they wait on one another at the barriers
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, moe_kernel<F>, p);
+}
+
+}  // namespace
+
+size_t moe_buffer_bytes(int M, int d, int f, int E, int k) {
+  size_t n = 0;
+  for (MoeFormat fmt : {MoeFormat::BF16, MoeFormat::F32, MoeFormat::MX4})
+    n = std::max(n, make_plan(M, d, f, E, k, fmt).total);
+  return n;
+}
+
+cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
+  const MoePlan pl = make_plan(a.M, a.d, a.f, a.E, a.k, a.format);
+  unsigned char* buf = static_cast<unsigned char*>(a.buf);
+  MParams p{};
+  p.x = a.x;
+  p.wr = a.Wr;
+  p.gu = static_cast<const uint8_t*>(a.W_gu);
+  p.gus = static_cast<const uint8_t*>(a.S_gu);
+  p.dn = static_cast<const uint8_t*>(a.W_d);
+  p.dns = static_cast<const uint8_t*>(a.S_d);
+  p.y = a.y;
+  p.idx = a.idx;
+  p.gate = a.gate;
+  p.sync = a.sync;
+  p.logits = reinterpret_cast<double*>(buf + pl.logits);
+  p.xop = buf + pl.xop;
+  p.hop = buf + pl.hop;
+  p.part1 = reinterpret_cast<float*>(buf + pl.part1);
+  p.part2 = reinterpret_cast<float*>(buf + pl.part2);
+  p.M = a.M;
+  p.d = a.d;
+  p.f = a.f;
+  p.E = a.E;
+  p.k = a.k;
+  p.cap1 = pl.cap1;
+  p.cap2 = pl.cap2;
+  p.renormalize = a.renormalize ? 1 : 0;
+  p.x_f32 = a.x_elem == Elem::F32 ? 1 : 0;
+  p.dev_status = a.dev_status;
+  p.wait_ns = wait_limit_ns();
+  switch (a.format) {
+    case MoeFormat::BF16: return launch_fmt<Fmt::BF16>(p, stream);
+    case MoeFormat::F32: return launch_fmt<Fmt::F32>(p, stream);
+    default: return launch_fmt<Fmt::MX4>(p, stream);
+  }
+}
+
+}  // namespace larosa

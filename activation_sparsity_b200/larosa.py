@@ -58,6 +58,8 @@ _SIGNATURES = {
     "larosa_mx4_linear": ([_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp], _i),
     "larosa_mx4_sparse_linear": ([_vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
     "larosa_mx4_topk_linear": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
+    "larosa_moe_layer": ([_vp] * 6 + [_i] * 6 + [_vp] * 4 + [_sz, _vp, _i, _vp], _i),
+    "larosa_moe_workspace_bytes": ([_i, _i, _i, _i, _i], _sz),
     "larosa_workspace_sync_offset": ([_i, _i, _i, _i, _c.POINTER(_sz)], _i),
     "larosa_set_wait_limit_ns": ([_c.c_uint64, _c.POINTER(_c.c_uint64)], _i),
     "larosa_set_debug": ([_i, _c.POINTER(_i)], _i),
@@ -88,6 +90,8 @@ LAROSA_MAX_M = 16
 LAROSA_MAX_D = 32768
 LAROSA_MX4_BLOCK = 32
 LAROSA_MX4_MAX_M = 1048576
+LAROSA_MOE_MAX_E = 512
+LAROSA_MOE_MAX_K = 16
 LAROSA_NOALLOC_SCRATCH_BYTES = 2 << 20
 
 
@@ -147,16 +151,22 @@ class Workspace:
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
             else torch.device(device)
         self.buf = torch.zeros(0, dtype=torch.uint8, device=self.device)
-        self._need: dict[tuple[int, int, int, int], int] = {}
+        self._need: dict[tuple[int, ...], int] = {}  # 4 sizes: get; 5: get_moe
 
     def get(self, M: int, d_in: int, d_out: int, K: int) -> torch.Tensor:
-        key = (M, d_in, d_out, K)
+        return self._sized(_lib.larosa_workspace_bytes, "larosa_workspace_bytes", (M, d_in, d_out, K))
+
+    def get_moe(self, M: int, d: int, f: int, E: int, k: int) -> torch.Tensor:
+        """The buffer for larosa_moe_layer of these sizes."""
+        return self._sized(_lib.larosa_moe_workspace_bytes, "larosa_moe_workspace_bytes", (M, d, f, E, k))
+
+    def _sized(self, query, name: str, key: tuple) -> torch.Tensor:
         need = self._need.get(key)
         if need is None:
             with torch.cuda.device(self.device):
-                need = int(_lib.larosa_workspace_bytes(M, d_in, d_out, K))
+                need = int(query(*key))
             if need == 0:
-                raise LarosaError(2, "larosa_workspace_bytes")
+                raise LarosaError(2, name)
             self._need[key] = need
         if self.buf.numel() < need:
             self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
@@ -597,7 +607,10 @@ def _ws_pair(ws, device: torch.device, *sizes) -> tuple[int, int]:
     tensor, or None for the current stream's own."""
     if ws is None:
         ws = default_workspace(device)
-    buf = ws.get(*sizes) if isinstance(ws, Workspace) else ws
+    if isinstance(ws, Workspace):
+        buf = ws.get(*sizes) if len(sizes) == 4 else ws.get_moe(*sizes)
+    else:
+        buf = ws
     if buf.device != device:
         raise ValueError(f"the workspace is on {buf.device}, the other tensors are on {device}")
     return buf.data_ptr(), buf.numel() * buf.element_size()
@@ -720,6 +733,56 @@ def larosa_mx4_topk_linear(x_rot: torch.Tensor, W_codes: torch.Tensor, W_scales:
     _call(_lib.larosa_mx4_topk_linear, "larosa_mx4_topk_linear", dev, x_rot.data_ptr(), W_codes.data_ptr(),
           W_scales.data_ptr(), M, d_in, d_out, K, y.data_ptr(), p, n, _status_word(dev_status, dev))
     return y
+
+
+def larosa_moe_workspace_bytes(M: int, d: int, f: int, E: int, k: int) -> int:
+    return int(_lib.larosa_moe_workspace_bytes(M, d, f, E, k))
+
+
+def larosa_moe_layer(x: torch.Tensor, Wr: torch.Tensor, W_gu: torch.Tensor, W_d: torch.Tensor, k: int,
+                     S_gu: torch.Tensor | None = None, S_d: torch.Tensor | None = None, renormalize: bool = True,
+                     y: torch.Tensor | None = None, idx: torch.Tensor | None = None,
+                     gate: torch.Tensor | None = None, ws=None, dev_status: torch.Tensor | None = None
+                     ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """A mixture-of-experts layer of a few tokens in one kernel: (y fp32 [M, d],
+    idx int32 [M, k], gate fp32 [M, k]).
+
+    x [M, d], router Wr [E, d], experts W_gu [E, d, 2 f] (gate | up) and W_d
+    [E, f, d] of x's type; or 4-bit experts, W_gu and W_d the codes and S_gu, S_d
+    the scales of larosa_mx4_quantize(W, axis=0)."""
+    _need(x, "x")
+    dev, dt = x.device, x.dtype
+    x = _as2d(x)
+    M, d = x.shape
+    code = _dtype_code(x)
+    _need_fast(Wr, "Wr", dt, dev)
+    if (S_gu is None) != (S_d is None):
+        raise ValueError("S_gu and S_d go together")
+    if W_gu.dim() != 3 or W_d.dim() != 3 or Wr.dim() != 2:
+        raise ValueError("Wr must be [E, d], W_gu [E, d, 2 f], W_d [E, f, d]")
+    E, f = W_d.shape[0], W_d.shape[1]
+    if S_gu is None:
+        _need_fast(W_gu, "W_gu", dt, dev)
+        _need_fast(W_d, "W_d", dt, dev)
+        ok = W_gu.shape == (E, d, 2 * f) and W_d.shape[2] == d
+        sg = sd = 0
+    else:
+        for t, name in ((W_gu, "W_gu"), (W_d, "W_d"), (S_gu, "S_gu"), (S_d, "S_d")):
+            _need_fast(t, name, torch.uint8, dev)
+        b = LAROSA_MX4_BLOCK
+        ok = (W_gu.shape == (E, d, f) and 2 * W_d.shape[2] == d and S_gu.shape == (E, d // b, 2 * f)
+              and S_d.shape == (E, f // b, d))
+        sg, sd = S_gu.data_ptr(), S_d.data_ptr()
+    if not ok or Wr.shape != (E, d):
+        raise ValueError("shapes of x, Wr, the experts and their scales do not agree")
+    y = _out(y, "y", (M, d), torch.float32, dev)
+    idx = _out(idx, "idx", (M, k), torch.int32, dev)
+    gate = _out(gate, "gate", (M, k), torch.float32, dev)
+    p, n = _ws_pair(ws, dev, M, d, f, E, k)
+    _call(_lib.larosa_moe_layer, "larosa_moe_layer", dev, x.data_ptr(), Wr.data_ptr(), W_gu.data_ptr(), sg,
+          W_d.data_ptr(), sd, M, d, f, E, k, 1 if renormalize else 0, y.data_ptr(), idx.data_ptr(), gate.data_ptr(),
+          p, n, _status_word(dev_status, dev), code)
+    return y, idx, gate
 
 
 def larosa_check(dev_status: torch.Tensor | None = None, device=None) -> int:

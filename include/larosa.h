@@ -80,6 +80,8 @@ typedef struct CUstream_st *larosa_stream_t;
 #define LAROSA_MAX_D 32768
 #define LAROSA_MX4_BLOCK 32 /* values that share a scale in the 4-bit format */
 #define LAROSA_MX4_MAX_M 1048576 /* tokens of larosa_mx4_linear */
+#define LAROSA_MOE_MAX_E 512 /* experts of larosa_moe_layer */
+#define LAROSA_MOE_MAX_K 16  /* experts per token */
 
 /* Return codes. */
 typedef enum {
@@ -480,7 +482,42 @@ int larosa_mx4_topk_linear(const float *x_rot, const void *W_codes,
                            int *dev_status, larosa_stream_t stream);
 
 /*
- * Workspace bytes sufficient for every entry point above called with these
+ * A mixture-of-experts layer for a few tokens, in one kernel:
+ *   l[m][e] = sum_i x[m][i] * Wr[e][i]                        router scores
+ *   idx[m]  = the k experts of largest score, largest first; among equal
+ *             scores the lower index first
+ *   gate[m] = softmax of the scores over those k experts (renormalize = 1) or
+ *             over all E experts (renormalize = 0), at idx[m]
+ *   h       = silu(x[m] . Wg) * (x[m] . Wu),  silu(v) = v / (1 + exp(-v))
+ *   y[m]    = sum_s gate[m][s] * (h . Wd)           Wg, Wu, Wd of idx[m][s]
+ * x: [M x d] and Wr: [E x d] of `dtype`; the experts row-major like the other
+ * x . W weights: W_gu [E x d x 2 f] = Wg | Wu along the columns, W_d
+ * [E x f x d].  With S_gu = S_d = NULL they are of `dtype`; otherwise they are
+ * 4-bit codes with scales S_gu and S_d (larosa_mx4_quantize with axis 0 of the
+ * E d x 2 f and the E f x d matrix), d and f multiples of 32.  y: [M x d] fp32;
+ * idx: [M x k] int32 and gate: [M x k] fp32, each may be NULL.  Scores are
+ * summed in fp64, everything else in fp32; results repeat bit for bit.  Only
+ * the chosen experts' weights are read.
+ * 1 <= M <= LAROSA_MAX_M, d and f multiples of 8, at most LAROSA_MAX_D,
+ * 1 <= k <= E, E <= LAROSA_MOE_MAX_E, k <= LAROSA_MOE_MAX_K; pointers 16-byte
+ * aligned.  A NaN or Inf among the scores sets LAROSA_DEV_NONFINITE; that
+ * token's outputs are then unspecified (the indices within [0, E)).
+ * ws: at least larosa_moe_workspace_bytes(M, d, f, E, k) bytes, zero-filled
+ * before its first use; it holds counters that are zero between calls, so
+ * calls sharing a workspace must not overlap.  The grid waits for itself
+ * twice, within the wait limit (LAROSA_DEV_TIMEOUT beyond it).
+ */
+int larosa_moe_layer(const void *x, const void *Wr, const void *W_gu,
+                     const void *S_gu, const void *W_d, const void *S_d, int M,
+                     int d, int f, int E, int k, int renormalize, float *y,
+                     int32_t *idx, float *gate, void *ws, size_t ws_bytes,
+                     int *dev_status, int dtype, larosa_stream_t stream);
+
+/* Workspace bytes of larosa_moe_layer (0 for out-of-range sizes). */
+size_t larosa_moe_workspace_bytes(int M, int d, int f, int E, int k);
+
+/*
+ * Workspace bytes sufficient for every entry point above that takes these
  * sizes (M tokens, d_in inputs, d_out outputs, K kept).  Returns 0 for
  * out-of-range sizes.
  */

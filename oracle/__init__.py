@@ -36,6 +36,7 @@ Functions and the passages they follow (page title, section):
 * ``mx4_quantize``, ``mx4_values``  the microscaled 4-bit storage of weights and
                         activations (the Open Compute Project's MXFP4): not on
                         the pages.
+* ``moe_layer``         a mixture-of-experts layer: not on the pages.
 
 Readings where the pages are silent:
 
@@ -63,4 +64,5 @@ from .larosa_ref import (  # noqa: F401
     sparse_lowrank_linear,
     mx4_quantize,
     mx4_values,
+    moe_layer,
 )

@@ -262,3 +262,29 @@ def mx4_values(codes, scales, axis: int) -> np.ndarray:
     v = E2M1[codes & 7] * np.where(codes & 8, -1.0, 1.0)
     s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales - 127))
     return v * np.repeat(s, 32, axis=axis)
+
+
+def moe_layer(x, Wr, W_gu, W_d, k: int, renormalize: bool):
+    """A mixture-of-experts layer, token by token: (y, idx, gate).
+
+    Not on the pages.  scores = Wr . x; the k largest (ties: the lower index),
+    largest first; gates = softmax of the scores over those k or over all
+    experts; y = sum_s gate_s (silu(x W_gate) * (x W_up)) W_down of expert s.
+    W_gu [E, d, 2 f] is gate | up along the columns, W_d [E, f, d].
+    """
+    x, Wr = np.asarray(x, dtype=np.float64), np.asarray(Wr, dtype=np.float64)
+    W_gu, W_d = np.asarray(W_gu, dtype=np.float64), np.asarray(W_d, dtype=np.float64)
+    M, f = x.shape[0], W_d.shape[1]
+    y = np.zeros_like(x)
+    idx, gate = np.empty((M, k), dtype=np.int64), np.empty((M, k))
+    for m in range(M):
+        scores = Wr @ x[m]
+        idx[m] = np.lexsort((np.arange(len(scores)), -scores))[:k]
+        top = scores[idx[m]]
+        over = top if renormalize else scores
+        gate[m] = np.exp(top - top[0]) / np.sum(np.exp(over - top[0]))
+        for s in range(k):
+            a = x[m] @ W_gu[idx[m, s]]
+            g, u = a[:f], a[f:]
+            y[m] += gate[m, s] * ((g / (1.0 + np.exp(-g)) * u) @ W_d[idx[m, s]])
+    return y, idx, gate

@@ -1,4 +1,4 @@
-"""What the 4-bit entry points refuse, on the host: no call here launches work."""
+"""What the 4-bit and expert entry points refuse, on the host: no call here launches work."""
 import ctypes
 
 import pytest
@@ -67,6 +67,26 @@ def test_linear(lib):
     assert f(MISALIGNED, FAKE, FAKE, FAKE, 4, 64, 64, FAKE, F32, None, None) == 3
     assert f(FAKE, FAKE, FAKE, MISALIGNED, 4, 64, 64, FAKE, F32, None, None) == 3
     assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, MISALIGNED, F32, None, None) == 3
+
+
+def test_moe_layer(lib):
+    f = lib.larosa_moe_layer
+    lib.larosa_moe_workspace_bytes.restype = ctypes.c_size_t
+
+    def call(x=FAKE, wr=FAKE, gu=FAKE, sg=None, dn=FAKE, sd=None, M=2, d=64, ff=96, E=8, k=2, re=1, y=FAKE, ws=FAKE,
+             nb=1 << 30, dt=BF16):
+        return f(x, wr, gu, sg, dn, sd, M, d, ff, E, k, re, y, None, None, ws, ctypes.c_size_t(nb), None, dt, None)
+
+    assert call(dt=3) == 4
+    assert call(x=None) == 1 and call(wr=None) == 1 and call(dn=None) == 1 and call(y=None) == 1
+    assert call(sg=FAKE) == 1 and call(sd=FAKE) == 1 and call(re=2) == 1
+    assert call(M=0) == 2 and call(M=17) == 2 and call(d=0) == 2 and call(d=32776) == 2 and call(ff=32776) == 2
+    assert call(E=0) == 2 and call(E=513) == 2 and call(k=0) == 2 and call(k=9) == 2 and call(E=64, k=17) == 2
+    assert call(d=60) == 3 and call(ff=100) == 3 and call(sg=FAKE, sd=FAKE, d=72) == 3
+    assert call(gu=MISALIGNED) == 3 and call(y=MISALIGNED) == 3
+    need = lib.larosa_moe_workspace_bytes(2, 64, 96, 8, 2)
+    assert need > 0 and lib.larosa_moe_workspace_bytes(2, 64, 96, 8, 9) == 0
+    assert call(ws=None) == 6 and call(nb=need - 1) == 6 and call(ws=MISALIGNED) == 6
 
 
 def test_binding_refuses_host_tensors_and_wrong_shapes():
