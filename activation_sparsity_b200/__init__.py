@@ -22,7 +22,7 @@ _EXPORTS = (
     "larosa_workspace_layout", "larosa_workspace_nnz_offset", "larosa_threshold",
     "larosa_rotate_threshold_linear", "larosa_fold_rotation",
     "larosa_sparse_lowrank_linear", "larosa_lowrank_workspace_bytes", "larosa_sparse_linear_noalloc_bytes",
-    "larosa_mx4_quantize", "larosa_mx4_dequantize", "larosa_mx4_linear",
+    "larosa_mx4_quantize", "larosa_mx4_dequantize", "larosa_mx4_linear", "larosa_mx4_linear_workspace_bytes",
     "larosa_mx4_sparse_linear", "larosa_mx4_topk_linear",
     "larosa_moe_layer", "larosa_moe_workspace_bytes",
     "LAROSA_MX4_BLOCK", "LAROSA_MX4_MAX_M", "LAROSA_MOE_MAX_E", "LAROSA_MOE_MAX_K",

@@ -1033,19 +1033,32 @@ int larosa_mx4_dequantize(const void* codes, const void* scales, int rows, int c
   return e == cudaSuccess ? LAROSA_OK : cuda_fail(e, "dequantise kernel");
 }
 
+static int check_mx4_linear(int M, int d_in, int d_out) {
+  if (M < 1 || M > LAROSA_MX4_MAX_M || d_in < 1 || d_in > LAROSA_MAX_D || d_out < 1 || d_out > kMaxDout)
+    return LAROSA_ERR_SHAPE;
+  return d_in % LAROSA_MX4_BLOCK == 0 ? LAROSA_OK : LAROSA_ERR_ALIGN;
+}
+
+size_t larosa_mx4_linear_workspace_bytes(int M, int d_in, int d_out) {
+  if (check_mx4_linear(M, d_in, d_out) != LAROSA_OK) return 0;
+  return align_up(kHeaderEnd, 256) + larosa::mx4_linear_buffer_bytes(M, d_in, d_out);
+}
+
 int larosa_mx4_linear(const void* x_codes, const void* x_scales, const void* Wt_codes, const void* Wt_scales, int M,
-                      int d_in, int d_out, void* y, int dtype, int* dev_status, larosa_stream_t stream) {
+                      int d_in, int d_out, void* y, void* ws, size_t ws_bytes, int* dev_status, int dtype,
+                      larosa_stream_t stream) {
   if (!valid_dtype(dtype)) return LAROSA_ERR_UNSUPPORTED_DTYPE;
   if (x_codes == nullptr || x_scales == nullptr || Wt_codes == nullptr || Wt_scales == nullptr || y == nullptr)
     return LAROSA_ERR_INVALID_ARG;
-  if (M < 1 || M > LAROSA_MX4_MAX_M || d_in < 1 || d_in > LAROSA_MAX_D || d_out < 1 || d_out > kMaxDout)
-    return LAROSA_ERR_SHAPE;
-  if (d_in % LAROSA_MX4_BLOCK != 0 || !aligned16(x_codes) || !aligned16(x_scales) || !aligned16(Wt_codes) ||
-      !aligned16(Wt_scales) || !aligned16(y))
+  const int st = check_mx4_linear(M, d_in, d_out);
+  if (st != LAROSA_OK) return st;
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(Wt_codes) || !aligned16(Wt_scales) || !aligned16(y))
     return LAROSA_ERR_ALIGN;
-  const cudaError_t e =
-      larosa::launch_mx4_linear(x_codes, x_scales, Wt_codes, Wt_scales, M, d_in, d_out, y, dtype == LAROSA_BF16,
-                                dev_status, reinterpret_cast<cudaStream_t>(stream));
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < larosa_mx4_linear_workspace_bytes(M, d_in, d_out))
+    return LAROSA_ERR_WORKSPACE;
+  const cudaError_t e = larosa::launch_mx4_linear(x_codes, x_scales, Wt_codes, Wt_scales, M, d_in, d_out, y,
+                                                  dtype == LAROSA_BF16, at(ws, align_up(kHeaderEnd, 256)), dev_status,
+                                                  reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LAROSA_OK : cuda_fail(e, "4-bit product kernel");
 }
 

@@ -294,10 +294,21 @@ cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, void* b
                             cudaStream_t stream);
 
 // Product of two MX4 matrices with blocks along d_in: y [M x d_out] =
-// x [M x d_in] . W^T, W [d_out x d_in] (mx4_linear.cu, tcgen05).
+// x [M x d_in] . W^T, W [d_out x d_in] (mx4_linear.cu, tcgen05).  buf:
+// mx4_linear_buffer_bytes of scratch.
 cudaError_t launch_mx4_linear(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
-                              int M, int d_in, int d_out, void* y, bool out_bf16, int* dev_status,
+                              int M, int d_in, int d_out, void* y, bool out_bf16, void* buf, int* dev_status,
                               cudaStream_t stream);
+size_t mx4_linear_buffer_bytes(int M, int d_in, int d_out);
+
+// The same on pairs of SMs with tiles of nt = 128, 192 or 256 tokens
+// (mx4_pair.cu), with mx4_pair_buffer_bytes of scratch, and the clocks a
+// shape is expected to take there.
+cudaError_t launch_mx4_pair(int nt, const void* x_codes, const void* x_scales, const void* w_codes,
+                            const void* w_scales, int M, int d_in, int d_out, void* y, bool out_bf16, void* buf,
+                            int* dev_status, cudaStream_t stream);
+size_t mx4_pair_buffer_bytes(int M, int d_in, int d_out);
+double mx4_pair_clocks(int nt, int M, int d_in, int d_out);
 
 // A mixture-of-experts layer for 1 to 16 tokens in one cooperative launch
 // (moe.cu).  W_gu [E][d][2 f], W_d [E][f][d] in `format` (MX4: codes, with

@@ -28,8 +28,9 @@
 // distributed shared memory in rank order, so results do not depend on
 // timing.  Every wait is bounded, as in the other tensor-core kernels.
 //
-// Tokens vary fastest over the grid: the CTAs at work share a few weight
-// tiles, and all of x lies in L2.
+// This kernel takes up to 64 tokens per tile; from there on pairs of SMs
+// share a tile (mx4_pair.cu).  Tokens vary fastest over the grid, so the CTAs
+// at work share weight tiles.
 #include <cooperative_groups.h>
 #include <cuda.h>
 
@@ -38,7 +39,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"
-#include "tcgen05.cuh"
+#include "mx4_umma.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -47,26 +48,25 @@ namespace {
 
 constexpr int kLThreads = 192;  // warps 0-3: scales, then epilogue; 4: TMA; 5: MMA
 constexpr int kRows = 128;      // outputs per CTA
-constexpr int kStageK = 256;    // inputs per stage
-constexpr int kStageBlocks = kStageK / mx4::kBlock;
 constexpr int kAhead = 4;       // stages whose scales are in flight
+using mx4::kStageBlocks;
+using mx4::kStageK;
 
 template <int NT>
 struct LCfg {
-  static constexpr int kHalves = (NT + 127) / 128;  // 128-token groups of scales
-  static constexpr int kStages = NT == 256 ? 4 : NT == 128 ? 6 : NT == 16 ? 5 : 4;
-  static constexpr int kPerSm = NT >= 128 ? 1 : 2;  // CTAs an SM holds
+  static constexpr int kStages = NT == 16 ? 5 : 4;
+  static constexpr int kPerSm = 2;  // CTAs an SM holds
   static constexpr uint32_t kA = kRows * 128, kB = NT * 128;
-  static constexpr uint32_t kSfA = 1024, kSfB = 1024 * kHalves;
+  static constexpr uint32_t kSfA = 1024, kSfB = 1024;
   static constexpr uint32_t kStage = kA + kB + kSfA + kSfB;
-  static constexpr int kSfCols = 8 + 8 * kHalves;  // TMEM columns of a stage's scales
+  static constexpr int kSfCols = 8 + 8;  // TMEM columns of a stage's scales
   static constexpr int kD = NT < 32 ? 32 : NT;
   static constexpr int kTmemUsed = kD + kStages * kSfCols;
   static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
   static_assert(kStage % 1024 == 0, "swizzled stages stay 1024-byte aligned");
   static_assert(kTmemUsed <= 512 && kPerSm * kTmemCols <= 512, "TMEM");
-  static_assert((size_t)std::min(NT, 64) * kRows * 4 <= (size_t)kStages * kStage, "partials fit the ring");
+  static_assert((size_t)NT * kRows * 4 <= (size_t)kStages * kStage, "partials fit the ring");
 };
 
 struct LParams {
@@ -79,43 +79,6 @@ struct LParams {
   int* dev_status;
   unsigned long long wait_ns;
 };
-
-// Instruction descriptor of kind::mxf4: A and B e2m1 (1), K-major, scales
-// ue8m0, M = 128, N = n; sf selects which half of a scale word the 64 inputs
-// take (0: bytes 0-1, 2: bytes 2-3).
-constexpr uint32_t idesc_mxf4(int n, int sf) {
-  return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(kRows >> 7) << 27) | ((uint32_t)sf << 29);
-}
-
-__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sfa, uint32_t sfb,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-
-// 512 bytes of scales (32 rows of 16 bytes) to four TMEM columns, in every
-// warp's lanes.  Descriptor: no swizzle, groups of eight rows 128 bytes apart.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr) {
-  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) |
-                        ((uint64_t)1 << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
-
-// Eight scale bytes of a row from block kb on; zeros past the row's end.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int blocks, int kb) {
-  if (row == nullptr || kb >= blocks) return make_uint2(0u, 0u);
-  if ((blocks & 7) == 0) return __ldg(reinterpret_cast<const uint2*>(row + kb));  // rows 8-byte aligned
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (kb + i < blocks) w[i >> 2] |= (uint32_t)__ldg(row + kb + i) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
-}
 
 __device__ __forceinline__ void store_out(const LParams& p, size_t at, float v) {
   if (p.out_bf16)
@@ -174,16 +137,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
     // ---------------------------------------------------------------- scales
     const int blocks = p.d_in / mx4::kBlock;
     const uint8_t* wrow = j0 + tid < p.d_out ? p.ws + (size_t)(j0 + tid) * blocks : nullptr;
-    const uint8_t* xrow[C::kHalves];
-#pragma unroll
-    for (int h = 0; h < C::kHalves; ++h)
-      xrow[h] = 128 * h + tid < NT && n0 + 128 * h + tid < p.M ? p.xs + (size_t)(n0 + 128 * h + tid) * blocks : nullptr;
-    uint2 a[kAhead], b[kAhead][C::kHalves];
+    const uint8_t* xrow = tid < NT && n0 + tid < p.M ? p.xs + (size_t)(n0 + tid) * blocks : nullptr;
+    uint2 a[kAhead], b[kAhead];
     auto load = [&](int it, int u) {
       const int kb = it < n_it ? (it0 + it) * kStageBlocks : blocks;
-      a[u] = load_scales(wrow, blocks, kb);
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h) b[u][h] = load_scales(xrow[h], blocks, kb);
+      a[u] = mx4::load_scales(wrow, blocks, kb);
+      b[u] = mx4::load_scales(xrow, blocks, kb);
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) load(u, u);
@@ -207,11 +166,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
         unsigned char* sfb = sfa + C::kSfA;
         *reinterpret_cast<uint32_t*>(sfa + at) = a[u].x;
         *reinterpret_cast<uint32_t*>(sfa + 512 + at) = a[u].y;
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-          *reinterpret_cast<uint32_t*>(sfb + 512 * h + at) = b[u][h].x;
-          *reinterpret_cast<uint32_t*>(sfb + 512 * (C::kHalves + h) + at) = b[u][h].y;
-        }
+        *reinterpret_cast<uint32_t*>(sfb + at) = b[u].x;
+        *reinterpret_cast<uint32_t*>(sfb + 512 + at) = b[u].y;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
@@ -250,15 +206,13 @@ __global__ void __launch_bounds__(kLThreads, 1)
         const uint32_t ta = tmem + C::kD + s * C::kSfCols, tb = ta + 8;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          copy_scales(ta + 4 * c, sfa + 512 * c);
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            copy_scales(tb + 4 * (c * C::kHalves + h), sfb + 512 * (c * C::kHalves + h));
+          mx4::copy_scales<1>(ta + 4 * c, sfa + 512 * c);
+          mx4::copy_scales<1>(tb + 4 * c, sfb + 512 * c);
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)  // 64 inputs (32 bytes) each
-          umma_mxf4(tmem, tc::sw128_desc(a_addr + kk * 32), tc::sw128_desc(b_addr + kk * 32),
-                    idesc_mxf4(NT, 2 * (kk & 1)), ta + 4 * (kk >> 1), tb + 4 * C::kHalves * (kk >> 1),
+          mx4::umma_mxf4<1>(tmem, tc::sw128_desc(a_addr + kk * 32), tc::sw128_desc(b_addr + kk * 32),
+                    mx4::idesc_mxf4(128, NT, 2 * (kk & 1)), ta + 4 * (kk >> 1), tb + 4 * (kk >> 1),
                     (it > 0 || kk > 0) ? 1u : 0u);
         tc::umma_commit(&empty[s]);  // the stage is free once these MMAs have read it
       }
@@ -314,7 +268,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     return;
   }
   // the splits' partial tiles, [token][output] in the (now idle) ring
-  if constexpr (NT <= 64) {
+  {
     cg::cluster_group cluster = cg::this_cluster();
     float* part = reinterpret_cast<float*>(stages);
     if (warp < 4) {
@@ -350,20 +304,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
   }
 }
 
-// A 2-D byte tensor map of a row-major [rows x bytes] matrix, box
-// [box_rows x 128 bytes], 128-byte swizzle.
-bool make_byte_map(CUtensorMap* map, const void* base, int rows, int bytes, int box_rows) {
-  const tc::EncodeTiled enc = tc::encoder();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)bytes};
-  const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int NT>
 cudaError_t launch_nt(const void* xc, const void* wc, LParams p, int R, cudaStream_t stream) {
   using C = LCfg<NT>;
@@ -381,7 +321,7 @@ cudaError_t launch_nt(const void* xc, const void* wc, LParams p, int R, cudaStre
     configured[dev] = 1;
   }
   CUtensorMap map_w, map_x;
-  if (!make_byte_map(&map_w, wc, p.d_out, p.d_in / 2, kRows) || !make_byte_map(&map_x, xc, p.M, p.d_in / 2, NT))
+  if (!mx4::make_byte_map(&map_w, wc, p.d_out, p.d_in / 2, kRows) || !mx4::make_byte_map(&map_x, xc, p.M, p.d_in / 2, NT))
     return cudaErrorInvalidValue;
   const int total = (p.d_in + kStageK - 1) / kStageK;
   p.stages_per_split = (total + R - 1) / R;
@@ -402,30 +342,38 @@ cudaError_t launch_nt(const void* xc, const void* wc, LParams p, int R, cudaStre
   return cudaLaunchKernelEx(&cfg, mx4_linear_kernel<NT>, map_w, map_x, p);
 }
 
-// Modelled time of a shape with NT tokens per tile and R splits: full waves
-// of CTAs times a CTA's stages (each costing its operand bytes) plus a fixed
-// part, in units of a 128-row stage.
+// Clocks of a shape with NT tokens per tile and R splits: full waves of CTAs
+// times a CTA's stages, each as long as its copies at 42 bytes per clock and
+// SM or its MMAs, and a fixed part.
 template <int NT>
-double tile_time(int M, int d_in, int d_out, int R) {
+double tile_clocks(int M, int d_in, int d_out, int R) {
   using C = LCfg<NT>;
   const int total = (d_in + kStageK - 1) / kStageK;
   const long long ctas = (long long)((M + NT - 1) / NT) * ((d_out + kRows - 1) / kRows) * R;
   const long long slots = 148LL * C::kPerSm;
   const long long waves = (ctas + slots - 1) / slots;
-  const double stage = std::max((128.0 + NT) / 144.0, NT / 64.0) * C::kPerSm;
-  return (double)waves * (((total + R - 1) / R) * stage + 8.0 + NT / 16.0);
+  const double stage = std::max(2.0 * NT, C::kStage / 42.0) * C::kPerSm;
+  return (double)waves * (((total + R - 1) / R) * stage + 4000.0 + 20.0 * NT);
 }
 
 }  // namespace
 
+// Tokens from which pairs of SMs are considered.
+constexpr int kPairTokens = 65;
+
+size_t mx4_linear_buffer_bytes(int M, int d_in, int d_out) {
+  return M < kPairTokens ? 0 : mx4_pair_buffer_bytes(M, d_in, d_out);
+}
+
 cudaError_t launch_mx4_linear(const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
-                              int M, int d_in, int d_out, void* y, bool out_bf16, int* dev_status,
+                              int M, int d_in, int d_out, void* y, bool out_bf16, void* buf, int* dev_status,
                               cudaStream_t stream) {
   LParams p{static_cast<const uint8_t*>(x_scales), static_cast<const uint8_t*>(w_scales), y, out_bf16 ? 1 : 0,
             M, d_in, d_out, 0, dev_status, wait_limit_ns()};
   const int total = (d_in + kStageK - 1) / kStageK;
-  // the tile and split that the model puts first; splits only of tiles of up
-  // to 64 tokens, at most 8 (the portable cluster size)
+  // The tile and split that the model puts first; splits only of tiles of up
+  // to 64 tokens, at most 8 (the portable cluster size).  Tiles of 128 tokens
+  // and more run on pairs of SMs (mx4_pair.cu).
   int nt = 0, R = 1;
   double best = 0.0;
   auto consider = [&](int n, int r, double t) {
@@ -436,18 +384,19 @@ cudaError_t launch_mx4_linear(const void* x_codes, const void* x_scales, const v
     }
   };
   for (int r = 1; r <= 8 && r <= total; r *= 2) {
-    if (M <= 16) consider(16, r, tile_time<16>(M, d_in, d_out, r));
-    consider(32, r, tile_time<32>(M, d_in, d_out, r));
-    if (M > 32) consider(64, r, tile_time<64>(M, d_in, d_out, r));
+    if (M <= 16) consider(16, r, tile_clocks<16>(M, d_in, d_out, r));
+    consider(32, r, tile_clocks<32>(M, d_in, d_out, r));
+    if (M > 32) consider(64, r, tile_clocks<64>(M, d_in, d_out, r));
   }
-  if (M > 64) consider(128, 1, tile_time<128>(M, d_in, d_out, 1));
-  if (M > 128) consider(256, 1, tile_time<256>(M, d_in, d_out, 1));
+  for (int n : {128, 192, 256})
+    if (M >= kPairTokens) consider(n, 1, mx4_pair_clocks(n, M, d_in, d_out));
   switch (nt) {
     case 16: return launch_nt<16>(x_codes, w_codes, p, R, stream);
     case 32: return launch_nt<32>(x_codes, w_codes, p, R, stream);
     case 64: return launch_nt<64>(x_codes, w_codes, p, R, stream);
-    case 128: return launch_nt<128>(x_codes, w_codes, p, 1, stream);
-    default: return launch_nt<256>(x_codes, w_codes, p, 1, stream);
+    default:
+      return launch_mx4_pair(nt, x_codes, x_scales, w_codes, w_scales, M, d_in, d_out, y, out_bf16, buf, dev_status,
+                             stream);
   }
 }
 

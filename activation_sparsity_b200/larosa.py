@@ -55,7 +55,8 @@ _SIGNATURES = {
     "larosa_sparse_linear_noalloc_bytes": ([_i, _i, _i, _i, _i], _sz),
     "larosa_mx4_quantize": ([_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp], _i),
     "larosa_mx4_dequantize": ([_vp, _vp, _i, _i, _i, _i, _vp, _vp], _i),
-    "larosa_mx4_linear": ([_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp], _i),
+    "larosa_mx4_linear": ([_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp, _i, _vp], _i),
+    "larosa_mx4_linear_workspace_bytes": ([_i, _i, _i], _sz),
     "larosa_mx4_sparse_linear": ([_vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
     "larosa_mx4_topk_linear": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp, _vp], _i),
     "larosa_moe_layer": ([_vp] * 6 + [_i] * 6 + [_vp] * 4 + [_sz, _vp, _i, _vp], _i),
@@ -151,17 +152,22 @@ class Workspace:
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
             else torch.device(device)
         self.buf = torch.zeros(0, dtype=torch.uint8, device=self.device)
-        self._need: dict[tuple[int, ...], int] = {}  # 4 sizes: get; 5: get_moe
+        self._need: dict[tuple[int, ...], int] = {}  # by the call's sizes
 
     def get(self, M: int, d_in: int, d_out: int, K: int) -> torch.Tensor:
         return self._sized(_lib.larosa_workspace_bytes, "larosa_workspace_bytes", (M, d_in, d_out, K))
+
+    def get_mx4_linear(self, M: int, d_in: int, d_out: int) -> torch.Tensor:
+        """The buffer for larosa_mx4_linear of these sizes."""
+        return self._sized(_lib.larosa_mx4_linear_workspace_bytes, "larosa_mx4_linear_workspace_bytes",
+                           (M, d_in, d_out))
 
     def get_moe(self, M: int, d: int, f: int, E: int, k: int) -> torch.Tensor:
         """The buffer for larosa_moe_layer of these sizes."""
         return self._sized(_lib.larosa_moe_workspace_bytes, "larosa_moe_workspace_bytes", (M, d, f, E, k))
 
     def _sized(self, query, name: str, key: tuple) -> torch.Tensor:
-        need = self._need.get(key)
+        need = self._need.get(key)  # the entry points differ in the number of sizes
         if need is None:
             with torch.cuda.device(self.device):
                 need = int(query(*key))
@@ -608,7 +614,7 @@ def _ws_pair(ws, device: torch.device, *sizes) -> tuple[int, int]:
     if ws is None:
         ws = default_workspace(device)
     if isinstance(ws, Workspace):
-        buf = ws.get(*sizes) if len(sizes) == 4 else ws.get_moe(*sizes)
+        buf = (ws.get if len(sizes) == 4 else ws.get_moe if len(sizes) == 5 else ws.get_mx4_linear)(*sizes)
     else:
         buf = ws
     if buf.device != device:
@@ -676,9 +682,13 @@ def larosa_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, axis: int =
     return out
 
 
+def larosa_mx4_linear_workspace_bytes(M: int, d_in: int, d_out: int) -> int:
+    return int(_lib.larosa_mx4_linear_workspace_bytes(M, d_in, d_out))
+
+
 def larosa_mx4_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, Wt_codes: torch.Tensor,
                       Wt_scales: torch.Tensor, dtype: torch.dtype = torch.float32, y: torch.Tensor | None = None,
-                      dev_status: torch.Tensor | None = None) -> torch.Tensor:
+                      ws=None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
     """y = x . W of two 4-bit matrices, [M, d_out] in `dtype`: x [M, d_in] and the
     weight in torch.nn.Linear layout [d_out, d_in], both of larosa_mx4_quantize
     with axis 1."""
@@ -690,9 +700,10 @@ def larosa_mx4_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, Wt_codes: t
     if x_codes.device != dev:
         raise ValueError(f"x_codes is on {x_codes.device}, the other tensors are on {dev}")
     y = _out(y, "y", (M, d_out), dtype if y is None else y.dtype, dev)
+    p, n = _ws_pair(ws, dev, M, d_in, d_out)
     _call(_lib.larosa_mx4_linear, "larosa_mx4_linear", dev, x_codes.data_ptr(), x_scales.data_ptr(),
-          Wt_codes.data_ptr(), Wt_scales.data_ptr(), M, d_in, d_out, y.data_ptr(), _dtype_code(y),
-          _status_word(dev_status, dev))
+          Wt_codes.data_ptr(), Wt_scales.data_ptr(), M, d_in, d_out, y.data_ptr(), p, n,
+          _status_word(dev_status, dev), _dtype_code(y))
     return y
 
 

@@ -442,13 +442,18 @@ int larosa_mx4_dequantize(const void *codes, const void *scales, int rows,
  * larosa_dense_linear), both held with axis 1.  On the tensor cores' 4-bit
  * rate; products exact, fp32 accumulation, y: [M x d_out] of `dtype` (bf16:
  * rounded once, to nearest even).  1 <= M <= LAROSA_MX4_MAX_M, d_in a multiple
- * of 32, d_out any; every pointer 16-byte aligned.  Uses no workspace;
- * results repeat bit for bit.
+ * of 32, d_out any; every pointer 16-byte aligned; results repeat bit for bit.
+ * ws: at least larosa_mx4_linear_workspace_bytes(M, d_in, d_out) bytes (from
+ * 65 tokens on it takes the scales in another order); calls sharing a
+ * workspace must not overlap.
  */
 int larosa_mx4_linear(const void *x_codes, const void *x_scales,
                       const void *Wt_codes, const void *Wt_scales, int M,
-                      int d_in, int d_out, void *y, int dtype, int *dev_status,
-                      larosa_stream_t stream);
+                      int d_in, int d_out, void *y, void *ws, size_t ws_bytes,
+                      int *dev_status, int dtype, larosa_stream_t stream);
+
+/* Workspace bytes of larosa_mx4_linear (0 for sizes it refuses). */
+size_t larosa_mx4_linear_workspace_bytes(int M, int d_in, int d_out);
 
 /*
  * larosa_sparse_linear with a 4-bit weight:

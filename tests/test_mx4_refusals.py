@@ -55,18 +55,19 @@ def test_sparse_and_topk_linear(lib):
 
 
 def test_linear(lib):
-    f = lib.larosa_mx4_linear
-    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, FAKE, 5, None, None) == 4
-    assert f(FAKE, None, FAKE, FAKE, 4, 64, 64, FAKE, F32, None, None) == 1
-    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, None, F32, None, None) == 1
-    assert f(FAKE, FAKE, FAKE, FAKE, 0, 64, 64, FAKE, F32, None, None) == 2
-    assert f(FAKE, FAKE, FAKE, FAKE, 1 << 21, 64, 64, FAKE, F32, None, None) == 2
-    assert f(FAKE, FAKE, FAKE, FAKE, 4, 65536, 64, FAKE, F32, None, None) == 2
-    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 0, FAKE, F32, None, None) == 2
-    assert f(FAKE, FAKE, FAKE, FAKE, 4, 72, 64, FAKE, F32, None, None) == 3
-    assert f(MISALIGNED, FAKE, FAKE, FAKE, 4, 64, 64, FAKE, F32, None, None) == 3
-    assert f(FAKE, FAKE, FAKE, MISALIGNED, 4, 64, 64, FAKE, F32, None, None) == 3
-    assert f(FAKE, FAKE, FAKE, FAKE, 4, 64, 64, MISALIGNED, F32, None, None) == 3
+    need = lib.larosa_mx4_linear_workspace_bytes
+    need.restype = ctypes.c_size_t
+
+    def call(xc=FAKE, xs=FAKE, wc=FAKE, ws_=FAKE, M=4, d_in=64, d_out=64, y=FAKE, ws=FAKE, nb=1 << 24, dt=F32):
+        return lib.larosa_mx4_linear(xc, xs, wc, ws_, M, d_in, d_out, y, ws, ctypes.c_size_t(nb), None, dt, None)
+
+    assert call(dt=5) == 4
+    assert call(xs=None) == 1 and call(wc=None) == 1 and call(y=None) == 1
+    assert call(M=0) == 2 and call(M=1 << 21) == 2 and call(d_in=65536) == 2 and call(d_out=0) == 2
+    assert call(d_in=72) == 3 and call(xc=MISALIGNED) == 3 and call(ws_=MISALIGNED) == 3 and call(y=MISALIGNED) == 3
+    assert call(ws=None) == 6 and call(ws=MISALIGNED) == 6
+    assert call(M=300, nb=need(300, 64, 64) - 1) == 6
+    assert need(300, 64, 64) > need(4, 64, 64) > 0 and need(4, 72, 64) == 0
 
 
 def test_moe_layer(lib):
