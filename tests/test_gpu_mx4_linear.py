@@ -47,7 +47,8 @@ def check(got, x, w, out):
 
 SHAPES = [(1, 32, 1), (1, 256, 128), (16, 256, 128), (3, 64, 40), (5, 512, 129), (17, 1024, 257), (33, 96, 130),
           (64, 2048, 384), (1, 4096, 1000), (7, 11008, 520), (16, 32768, 128), (65, 544, 127), (100, 288, 640),
-          (128, 4096, 256), (129, 1056, 200), (200, 640, 5000), (257, 800, 1111), (300, 8192, 260), (1000, 256, 20000)]
+          (128, 4096, 256), (129, 1056, 200), (200, 640, 5000), (257, 800, 1111), (300, 8192, 260), (1000, 256, 20000),
+          (640, 512, 3001), (2048, 96, 5000), (129, 64, 40000), (384, 1536, 10240), (2050, 288, 4104)]
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
