@@ -50,7 +50,7 @@
 //                    8 rows: at 60 % kept a block takes 24 of 32 slots.  One
 //                    or two warps abreast (128 or 256 columns per CTA) share
 //                    them;
-//   5 to 16 tokens   the operand is made once, by one CTA per token, and
+//   5 to 16 tokens   the operand is made once, by a few CTAs per token, and
 //                    copied along with the rows: making it in every column
 //                    tile would cost as much as the product.  Nearly every
 //                    row is kept by some token, so rows are not packed; one
@@ -110,15 +110,22 @@ __device__ __forceinline__ void reduce_tile(const float (&acc)[NT][8][2], float*
   __syncthreads();
   const int S = gridDim.x, tile = blockIdx.y, count = p.M * kCols;
   float* slab = p.partials + ((size_t)blockIdx.x * gridDim.y + tile) * count;
-  for (int e = tid; e < count; e += kRThreads) {
-    float s = part[e];
+  for (int e = tid; e < count / 4; e += kRThreads) {
+    const float4* from = reinterpret_cast<const float4*>(part) + e;
+    float4 s = *from;
 #pragma unroll
-    for (int w = 1; w < kRWarps / kHalves; ++w) s += part[w * kTok * kCols + e];
+    for (int w = 1; w < kRWarps / kHalves; ++w) {
+      const float4 v = from[w * kTok * kCols / 4];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
     if (S > 1) {
-      __stcg(slab + e, s);
+      __stcg(reinterpret_cast<float4*>(slab) + e, s);
     } else {
-      const int m = e / kCols, j = tile * kCols + e % kCols;
-      if (j < p.d_out) p.y[(size_t)m * p.d_out + j] = s;
+      const int m = 4 * e / kCols, j = tile * kCols + 4 * e % kCols;
+      if (j < p.d_out) *reinterpret_cast<float4*>(p.y + (size_t)m * p.d_out + j) = s;
     }
   }
   if (S == 1) return;
@@ -126,19 +133,25 @@ __device__ __forceinline__ void reduce_tile(const float (&acc)[NT][8][2], float*
   if (tid == 0) s_order = atomic_add_acq_rel_gpu(&p.tickets[tile], 1u);
   __syncthreads();
   if (s_order != (unsigned)S - 1u) return;
-  const size_t step = (size_t)gridDim.y * count;
-  for (int e = tid; e < count; e += kRThreads) {
-    const float* from = p.partials + (size_t)tile * count + e;
-    float s = 0.f;
-    for (int r0 = 0; r0 < S; r0 += 8) {  // eight loads in flight, added in split order
-      float v[8];
+  // four columns at a time, every split's in flight, added in split order
+  const size_t step = (size_t)gridDim.y * count / 4;
+  for (int e = tid; e < count / 4; e += kRThreads) {
+    const float4* from = reinterpret_cast<const float4*>(p.partials + (size_t)tile * count) + e;
+    float4 v[kMaxSplits];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r0 + i < S ? __ldcg(from + (size_t)(r0 + i) * step) : 0.f;
+    for (int i = 0; i < kMaxSplits; ++i)
+      v[i] = i < S ? __ldcg(from + (size_t)i * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 s = v[0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i];
+    for (int i = 1; i < kMaxSplits; ++i) {
+      s.x += v[i].x;
+      s.y += v[i].y;
+      s.z += v[i].z;
+      s.w += v[i].w;
     }
-    const int m = e / kCols, j = tile * kCols + e % kCols;
-    if (j < p.d_out) p.y[(size_t)m * p.d_out + j] = s;
+    const int m = 4 * e / kCols, j = tile * kCols + 4 * e % kCols;
+    // rows of y are multiples of 128 bytes, so a group of four is inside or outside
+    if (j < p.d_out) *reinterpret_cast<float4*>(p.y + (size_t)m * p.d_out + j) = s;
   }
   if (tid == 0) p.tickets[tile] = 0u;  // every split has arrived
 }
@@ -384,11 +397,11 @@ __global__ void __launch_bounds__(kRThreads, kManyCtas) mx4_rows_many_kernel(con
   pdl_wait();
   pdl_launch_dependents();
 
-  // rows of block b that some token keeps
-  auto kept_rows = [&](int b) -> unsigned {
-    const unsigned m = b < b_end && lane < p.M ? __ldg(p.op.mask + (size_t)b * kTok + lane) : 0u;
-    return __reduce_or_sync(0xffffffffu, m);
+  // this lane's token's kept rows of block b; all tokens' together
+  auto read_mask = [&](int b) -> unsigned {
+    return b < b_end && lane < p.M ? __ldg(p.op.mask + (size_t)b * kTok + lane) : 0u;
   };
+  auto any_token = [&](unsigned m) -> unsigned { return __reduce_or_sync(0xffffffffu, m); };
   auto copy = [&](int b, unsigned kept, int stage_no) {
     if (kept != 0u) {
       ManyTile<NT>& tile = ring[stage_no];
@@ -408,16 +421,21 @@ __global__ void __launch_bounds__(kRThreads, kManyCtas) mx4_rows_many_kernel(con
   };
 
   int b = b_begin + warp / kHalves;
-  // kept[s]: rows of the block in tile s of the ring, and of the one after
-  unsigned kept[kRing];
+  // kept[s]: rows of the block in tile s of the ring, and of the one after;
+  // masks are read two blocks before they are needed
+  unsigned kept[kRing], raw[kRing];
 #pragma unroll
-  for (int s = 0; s < kRing; ++s) kept[s] = kept_rows(b + s * kLanes);
+  for (int s = 0; s < kRing; ++s) raw[s] = read_mask(b + s * kLanes);
+  unsigned raw_next = read_mask(b + kRing * kLanes);
+#pragma unroll
+  for (int s = 0; s < kRing; ++s) kept[s] = any_token(raw[s]);
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) copy(b + s * kLanes, kept[s], s);
   for (int it = 0; b < b_end; b += kLanes, ++it) {
     __syncwarp();  // every lane has read the tile that is filled next
     copy(b + (kRing - 1) * kLanes, kept[kRing - 1], (it + kRing - 1) % kRing);
-    const unsigned after = kept_rows(b + kRing * kLanes);
+    const unsigned after = any_token(raw_next);
+    raw_next = read_mask(b + (kRing + 1) * kLanes);
     mx4::copies_wait<kRing - 1>();
     __syncwarp();  // the other lanes' copies too
     if (kept[0] != 0u) {
@@ -447,31 +465,47 @@ __global__ void __launch_bounds__(kRThreads, kManyCtas) mx4_rows_many_kernel(con
 
 constexpr int kPThreads = 1024;
 
-// One CTA per token scatters the kept list into a row of shared memory, then
-// writes it as a dense fp32 row (coef) or as the token's operand.
+// The CTAs of a token each scatter the entries of the kept list that fall
+// into their range of rows into shared memory, then write the range as a
+// dense fp32 row (coef) or as the token's operand.
+constexpr int kCoefParts = 4;
+
 __global__ void __launch_bounds__(kPThreads, 1)
     mx4_coef_kernel(const int32_t* __restrict__ idx, const float* __restrict__ val, int K, int d, float* coef,
                     mx4::Operand op, int* dev_status) {
   extern __shared__ __align__(16) float row[];
   const int m = blockIdx.x;
-  for (int i = threadIdx.x; i < d; i += kPThreads) row[i] = 0.f;
+  const int blocks = d / mx4::kBlock;
+  const int b0 = blockIdx.y * blocks / kCoefParts, b1 = (blockIdx.y + 1) * blocks / kCoefParts;
+  const unsigned first = (unsigned)b0 * 32u, rows = (unsigned)(b1 - b0) * 32u;
+  for (unsigned i = threadIdx.x; i < rows; i += kPThreads) row[i] = 0.f;
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   bool bad = false;
-  for (int k = threadIdx.x; k < K; k += kPThreads) {
-    const int i = __ldg(idx + (size_t)m * K + k);
-    if (static_cast<unsigned>(i) < static_cast<unsigned>(d))
-      row[i] = __ldg(val + (size_t)m * K + k);
-    else
-      bad = true;
+  constexpr int kBatch = 8;  // entries in flight per thread
+  for (int k0 = threadIdx.x; k0 < K; k0 += kBatch * kPThreads) {
+    unsigned r[kBatch];
+    float v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = k0 + i * kPThreads;
+      r[i] = k < K ? (unsigned)__ldg(idx + (size_t)m * K + k) : 0u;
+      v[i] = k < K ? __ldg(val + (size_t)m * K + k) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (k0 + i * kPThreads >= K) break;
+      if (r[i] - first < rows) row[r[i] - first] = v[i];
+      bad |= r[i] >= (unsigned)d;
+    }
   }
   if (__syncthreads_or(bad) && threadIdx.x == 0) report(dev_status, LAROSA_DEV_INDEX);
   if (coef != nullptr) {
-    for (int i = threadIdx.x; i < d; i += kPThreads) coef[(size_t)m * d + i] = row[i];
+    for (unsigned i = threadIdx.x; i < rows; i += kPThreads) coef[(size_t)m * d + first + i] = row[i];
   } else {
     const int lane = threadIdx.x & 31;
-    for (int b = threadIdx.x >> 5; b < d / mx4::kBlock; b += kPThreads / 32) op.put(b, m, row[b * 32 + lane], lane);
+    for (int b = b0 + (threadIdx.x >> 5); b < b1; b += kPThreads / 32) op.put(b, m, row[(b - b0) * 32 + lane], lane);
   }
 }
 
@@ -603,9 +637,9 @@ cudaError_t launch_mx4_coef(const int32_t* idx, const float* val, int M, int K, 
   cudaError_t e = allow_smem(mx4_coef_kernel, (size_t)LAROSA_MAX_D * 4, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(M, 1, 1);
+  cfg.gridDim = dim3(M, kCoefParts, 1);
   cfg.blockDim = dim3(kPThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)d_in * 4;
+  cfg.dynamicSmemBytes = (size_t)(d_in / mx4::kBlock + kCoefParts - 1) / kCoefParts * mx4::kBlock * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
