@@ -18,19 +18,22 @@
 // barriers, and a CTA asks for its first down rows to be brought into L2
 // before it waits at the second.
 //
-//   scores   a warp per expert and four tokens, summed in fp64: selection is
-//            a comparison, so scores that differ by less than fp32 rounding
-//            must not swap.  (Products of two fp32 values are exact in fp64.)
+//   scores   a CTA per expert and four tokens, its warps each a share of the
+//            inputs, summed in fp64: selection is a comparison, so scores that
+//            differ by less than fp32 rounding must not swap.  (Products of
+//            two fp32 values are exact in fp64.)
 //   routing  every CTA makes the same selection and the same work list from
 //            the scores.  A group is an expert and up to eight of its tokens.
-//   products a unit is a group, a tile of columns (gate and up halves side by
-//            side) and a split of the rows.  The CTA's eight warps take rows
-//            in turn, their sums are added in warp order in shared memory,
-//            the splits' (and for down also the experts') sums go through the
-//            workspace and the last unit of a tile to arrive adds them in a
-//            fixed order: results repeat bit for bit.  The number of splits
-//            follows from the number of groups, so that there are units for
-//            all CTAs.
+//   products a unit is a group and a tile of columns (gate and up halves side
+//            by side).  The rows of all units, in order, are one line of warp
+//            steps that is cut into equal shares, one per CTA: the number of
+//            units follows from the routing (5 tokens of 60 experts made 396
+//            units for 296 CTAs: whole units would take twice the time of
+//            equal shares).  A CTA's eight warps take steps in turn and add
+//            their sums in warp order in shared memory; where a unit (down: a
+//            column tile) spans CTAs, their sums go through the workspace and
+//            the last to arrive adds them in a fixed order, so results repeat
+//            bit for bit.
 //
 // The products run on mma.sync.m16n8k16 with fp32 accumulators: eight tokens
 // of fp32 FMAs per 2-byte weight would be the limit instead of HBM.  A lane
@@ -56,7 +59,7 @@ constexpr int kGroup = 8;      // tokens of a group
 constexpr int kMaxE = 512;     // LAROSA_MOE_MAX_E
 constexpr int kMaxK = 16;      // LAROSA_MOE_MAX_K
 constexpr int kMaxPairs = 16 * kMaxK;
-constexpr int kMaxSplits = 8;
+constexpr int kMaxParts = 16;  // CTAs a unit may span
 constexpr int kCtasPerSm = 2;
 
 enum class Fmt { BF16, F32, MX4 };
@@ -80,10 +83,9 @@ struct MParams {
   double* logits;        // [M][E]
   unsigned char* xop;    // MX4: x's pieces [M][2][d] f16, then scales [M][d / 32]
   unsigned char* hop;    // h: bf16 pieces [pairs][3][f], fp32 [pairs][f], or as xop
-  float* part1;          // [splits][pairs][2 f]
-  float* part2;          // [splits][pairs][d]
+  float* part1;          // [parts][pairs][2 f]
+  float* part2;          // [parts][pairs][d]
   int M, d, f, E, k;
-  int cap1, cap2;        // most splits the workspace holds
   int renormalize;
   int x_f32;             // MX4 experts: x and Wr are fp32
   int* dev_status;
@@ -92,7 +94,7 @@ struct MParams {
 
 // The routing of a call, the same in every CTA.
 struct Routing {
-  double top[16][kMaxK];
+  double sums[kWarps][4];  // scores: the warps' shares
   float gate[kMaxPairs];
   int expert[kMaxPairs];
   int cnt[kMaxE];
@@ -100,6 +102,7 @@ struct Routing {
   short g_expert[kMaxPairs];
   short g_n[kMaxPairs];
   short g_pair[kMaxPairs][kGroup];
+  short parts[kMaxPairs];  // down: CTAs that a group's unit of the current tile spans
   int groups;
   int ok;
   unsigned order;
@@ -157,20 +160,19 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// Warp tasks (expert, four tokens), dealt over the grid so that few tasks
-// land on many SMs.
+// Tasks (expert, four tokens), one CTA each.
 template <typename T>
-__device__ void scores(const MParams& p) {
-  const int lane = threadIdx.x & 31;
+__device__ void scores(const MParams& p, Routing* r) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tg = (p.M + 3) / 4;
   const T* x = static_cast<const T*>(p.x);
   const T* wr = static_cast<const T*>(p.wr);
-  for (int task = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; task < p.E * tg; task += kWarps * gridDim.x) {
+  for (int task = blockIdx.x; task < p.E * tg; task += gridDim.x) {
     const int e = task / tg, m0 = task % tg * 4;
     const T* w = wr + (size_t)e * p.d;
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 2
-    for (int i = lane * 8; i < p.d; i += 256) {
+    for (int i = threadIdx.x * 8; i < p.d; i += kT * 8) {
       float wv[8];
       load8<T>(w + i, wv);
 #pragma unroll
@@ -185,10 +187,20 @@ __device__ void scores(const MParams& p) {
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
+      if (m0 + m < p.M) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
-      if (lane == 0 && m0 + m < p.M) __stcg(p.logits + (size_t)(m0 + m) * p.E + e, acc[m]);
+        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
+        if (lane == 0) r->sums[warp][m] = acc[m];
+      }
     }
+    __syncthreads();
+    if (threadIdx.x < 4 && m0 + (int)threadIdx.x < p.M) {
+      double v = r->sums[0][threadIdx.x];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) v += r->sums[i][threadIdx.x];
+      __stcg(p.logits + (size_t)(m0 + threadIdx.x) * p.E + e, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -217,14 +229,21 @@ __device__ __forceinline__ unsigned long long score_key(double v) {
   return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
 
-// Selection and softmax of token m by one warp.
+// The score a key was made of (a NaN's comes back as NaN).
+__device__ __forceinline__ double key_score(unsigned long long k) {
+  if (k == 1ull) return __longlong_as_double(0x7ff8000000000000ll);
+  return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
+
+// Selection and softmax of token m by one warp; a lane holds kPer scores.
+template <int kPer>
 __device__ void route_token(const MParams& p, Routing* r, int m) {
   const int lane = threadIdx.x & 31;
   const double* l = p.logits + (size_t)m * p.E;
-  unsigned long long key[kMaxE / 32];
+  unsigned long long key[kPer];
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kMaxE / 32; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
     key[i] = 0ull;
     if (e < p.E) {
@@ -234,50 +253,101 @@ __device__ void route_token(const MParams& p, Routing* r, int m) {
     }
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) report(p.dev_status, LAROSA_DEV_NONFINITE);
+  float den = 0.f, mine = 0.f;    // lane s: exp of the s-th score's distance from the first
+  int expert = 0;
+  if (!p.renormalize) {
+    // the sum over every expert, before keys are taken out
+    unsigned long long best = 0ull;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) best = key[i] > best ? key[i] : best;
+    const unsigned mh = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32));
+    const unsigned ml = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32) == mh ? (unsigned)best : 0u);
+    const double top = key_score((unsigned long long)mh << 32 | ml);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < p.E) den += expf((float)(key_score(key[i]) - top));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  }
+  double score = 0.0;  // lane s: the s-th largest
   for (int s = 0; s < p.k; ++s) {
     unsigned long long best = 0ull;
     int at = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxE / 32; ++i)
+    for (int i = 0; i < kPer; ++i)
       if (key[i] > best) {
         best = key[i];
         at = i;
       }
+    // the largest upper halves, and only where several lanes share them the rest
     const unsigned hi = (unsigned)(best >> 32);
     const unsigned mh = __reduce_max_sync(0xffffffffu, hi);
-    const unsigned ml = __reduce_max_sync(0xffffffffu, hi == mh ? (unsigned)best : 0u);
-    const bool mine = hi == mh && (unsigned)best == ml;
-    const unsigned e = __reduce_min_sync(0xffffffffu, mine ? (unsigned)(lane + 32 * at) : 0xffffffffu);
+    const unsigned holders = __ballot_sync(0xffffffffu, hi == mh);
+    unsigned ml, e;
+    if (__popc(holders) == 1) {
+      const int from = __ffs(holders) - 1;
+      ml = __shfl_sync(0xffffffffu, (unsigned)best, from);
+      e = __shfl_sync(0xffffffffu, (unsigned)(lane + 32 * at), from);
+    } else {
+      ml = __reduce_max_sync(0xffffffffu, hi == mh ? (unsigned)best : 0u);
+      const bool has = hi == mh && (unsigned)best == ml;
+      e = __reduce_min_sync(0xffffffffu, has ? (unsigned)(lane + 32 * at) : 0xffffffffu);
+    }
 #pragma unroll
-    for (int i = 0; i < kMaxE / 32; ++i)
+    for (int i = 0; i < kPer; ++i)
       if ((unsigned)(lane + 32 * i) == e) key[i] = 0ull;
-    if (lane == 0) {
-      r->expert[m * p.k + s] = (int)e;
-      r->top[m][s] = __ldcg(l + e);
+    if (lane == s) {
+      score = key_score((unsigned long long)mh << 32 | ml);
+      expert = (int)e;
     }
   }
-  __syncwarp();
-  const double l0 = r->top[m][0];
-  float den = 0.f;
+  const double l0 = __shfl_sync(0xffffffffu, score, 0);
+  mine = lane < p.k ? expf((float)(score - l0)) : 0.f;
   if (p.renormalize) {
-    for (int s = 0; s < p.k; ++s) den += expf((float)(r->top[m][s] - l0));
-  } else {
-    for (int e = lane; e < p.E; e += 32) den += expf((float)(__ldcg(l + e) - l0));
+    den = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   }
-  for (int s = lane; s < p.k; s += 32) {
-    const float g = expf((float)(r->top[m][s] - l0)) / den;
-    r->gate[m * p.k + s] = g;
+  if (lane < p.k) {
+    const int q = m * p.k + lane;
+    r->expert[q] = expert;
+    r->gate[q] = mine / den;
     if (blockIdx.x == 0) {
-      if (p.idx != nullptr) p.idx[m * p.k + s] = r->expert[m * p.k + s];
-      if (p.gate != nullptr) p.gate[m * p.k + s] = g;
+      if (p.idx != nullptr) p.idx[q] = expert;
+      if (p.gate != nullptr) p.gate[q] = mine / den;
     }
   }
 }
 
-// The groups: experts in ascending order, each one's pairs (token, slot) in
-// ascending order, eight to a group.
+// The groups of up to 32 pairs (token, slot), by one warp: experts in the
+// order of their first pair, an expert's pairs in ascending order, eight to a
+// group.
+__device__ void build_groups_warp(const MParams& p, Routing* r) {
+  const int lane = threadIdx.x & 31;
+  const int pairs = p.M * p.k;
+  const int e = lane < pairs ? r->expert[lane] : -1;
+  const unsigned same = __match_any_sync(0xffffffffu, e);
+  const int rank = __popc(same & ((1u << lane) - 1u)), cnt = __popc(same);
+  const int n = lane < pairs && rank == 0 ? (cnt + kGroup - 1) / kGroup : 0;
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int base = __shfl_sync(0xffffffffu, incl - n, __ffs(same) - 1);
+  if (lane < pairs) {
+    const int g = base + rank / kGroup;
+    r->g_pair[g][rank % kGroup] = (short)lane;
+    if (rank % kGroup == 0) {
+      r->g_expert[g] = (short)e;
+      r->g_n[g] = (short)min(kGroup, cnt - rank);
+    }
+  }
+  if (lane == 31) r->groups = incl;
+}
+
+// The groups of more pairs, by the CTA: experts in ascending order.
 __device__ void build_groups(const MParams& p, Routing* r) {
   const int tid = threadIdx.x;
   const int pairs = p.M * p.k;
@@ -648,16 +718,41 @@ __device__ __forceinline__ bool last_to_arrive(unsigned* ticket, unsigned count,
   return r->order == count - 1u;
 }
 
-__device__ __forceinline__ int splits_for(int units, int steps, int cap) {
-  return max(1, min(min(cap, (int)gridDim.x / max(units, 1)), steps));
-}
+// The line of warp steps of a phase: `units` units of `steps` each, cut into
+// `ctas` shares.
+struct Line {
+  int steps;
+  long long total;
+  int ctas;
 
-// Rows [k0, k1) of split s of S: whole steps.
-__device__ __forceinline__ void split_rows(int rows, int step, int S, int s, int* k0, int* k1) {
-  const int steps = (rows + step - 1) / step;
-  *k0 = (int)((long long)steps * s / S) * step;
-  *k1 = min(rows, (int)((long long)steps * (s + 1) / S) * step);
-}
+  // A share is at least two steps per warp (a unit that one CTA can finish in
+  // that time is not worth a sum through the workspace), and a unit spans at
+  // most kMaxParts CTAs (a share is at least steps / (kMaxParts - 2)).
+  __host__ __device__ Line(int units, int steps_, int grid) : steps(steps_), total((long long)units * steps_) {
+    const long long by_share = total / (2 * kWarps), most = (long long)units * (kMaxParts - 2);
+    long long n = by_share < grid ? by_share : grid;
+    if (n > most) n = most;
+    ctas = n < 1 ? 1 : (int)n;
+  }
+  // a b / c; 32-bit division where the product allows it (a 64-bit one takes
+  // some hundred instructions)
+  static __device__ __forceinline__ long long mul_div(long long a, long long b, long long c) {
+    const long long n = a * b;
+    return n >> 32 == 0 ? (long long)((unsigned)n / (unsigned)c) : n / c;
+  }
+  __device__ __forceinline__ long long begin(int cta) const { return mul_div(total, cta, ctas); }
+  // The CTA whose share holds step `at`.
+  __device__ __forceinline__ int owner(long long at) const {
+    const long long n = (at + 1) * ctas - 1;
+    return n >> 32 == 0 ? (int)((unsigned)n / (unsigned)total) : (int)(n / total);
+  }
+  // Unit of step `at`.
+  __device__ __forceinline__ int unit(long long at) const {
+    return at >> 32 == 0 ? (int)((unsigned)at / (unsigned)steps) : (int)(at / steps);
+  }
+  // Most CTAs a unit can span.
+  int parts() const { return (int)((steps + total / ctas - 1) / (total / ctas)) + 1; }
+};
 
 template <Fmt F>
 __device__ __forceinline__ size_t row_bytes_of(int cols) {
@@ -678,9 +773,9 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   // ------------------------------------------------------------------ scores
   const bool x_f32 = F == Fmt::F32 || (F == Fmt::MX4 && p.x_f32);
   if (x_f32)
-    scores<float>(p);
+    scores<float>(p, &r);
   else
-    scores<__nv_bfloat16>(p);
+    scores<__nv_bfloat16>(p, &r);
   if constexpr (F == Fmt::MX4) {
     const int blocks = p.d / 32;
     for (int i = warp * gridDim.x + blockIdx.x; i < p.M * blocks; i += kWarps * gridDim.x) {
@@ -694,19 +789,36 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   if (!grid_barrier(p.sync + kSyncA, &r, p)) return;
 
   // ------------------------------------------------------------------ routing
-  for (int m = warp; m < p.M; m += kWarps) route_token(p, &r, m);
+  for (int m = warp; m < p.M; m += kWarps) {
+    if (p.E <= 32)
+      route_token<1>(p, &r, m);
+    else if (p.E <= 128)
+      route_token<4>(p, &r, m);
+    else
+      route_token<kMaxE / 32>(p, &r, m);
+  }
   __syncthreads();
-  build_groups(p, &r);
+  if (pairs <= 32) {
+    if (warp == 0) build_groups_warp(p, &r);
+    __syncthreads();
+  } else {
+    build_groups(p, &r);
+  }
   const int G = r.groups;
 
   // ------------------------------------------------------------------ gate | up
   float* part = reinterpret_cast<float*>(smem);
   {
     const int tiles = (p.f + kSeg - 1) / kSeg;
-    const int S = splits_for(G * tiles, (p.d + kStep * kWarps - 1) / (kStep * kWarps), p.cap1);
+    const Line line(G * tiles, (p.d + kStep - 1) / kStep, gridDim.x);
     const size_t expert_bytes = row_bytes_of<F>(2 * p.f) * p.d;
-    for (int w = blockIdx.x; w < G * tiles * S; w += gridDim.x) {
-      const int group = w % G, split = w / G % S, tile = w / G / S;
+    const int me = blockIdx.x;
+    long long at = me < line.ctas ? line.begin(me) : 0;
+    const long long stop = me < line.ctas ? line.begin(me + 1) : 0;
+    while (at < stop) {
+      const int w = line.unit(at), s0 = (int)(at - (long long)w * line.steps);
+      const int s1 = (int)min((long long)line.steps, s0 + (stop - at));
+      const int group = w % G, tile = w / G;
       const int e = r.g_expert[group];
       Unit u;
       u.W = p.gu + (size_t)e * expert_bytes;
@@ -717,9 +829,11 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
       u.cB = p.f + tile * kSeg;
       u.wA = u.wB = min(kSeg, p.f - tile * kSeg);
       u.n = r.g_n[group];
-      split_rows(p.d, kStep, S, split, &u.k0, &u.k1);
+      u.k0 = s0 * kStep;
+      u.k1 = min(p.d, s1 * kStep);
       unit_product<F, false>(p, &r, group, u, smem);
-      if (S == 1) {
+      at += s1 - s0;
+      if (s0 == 0 && s1 == line.steps) {
         for (int i = tid; i < u.n * kSeg; i += kT) {
           const int pos = i / kSeg, j = i % kSeg;
           if (j < u.wA)
@@ -727,30 +841,36 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
         }
         continue;
       }
+      // the unit spans CTAs first ... first + parts - 1
+      const int first = line.owner((long long)w * line.steps);
+      const int parts = line.owner((long long)(w + 1) * line.steps - 1) - first + 1;
       for (int i = tid; i < u.n * kCols; i += kT) {
         const int pos = i / kCols, c = i % kCols, j = c % kSeg;
         if (j < u.wA)
-          __stcg(p.part1 + ((size_t)split * pairs + r.g_pair[group][pos]) * (2 * p.f) + (c < kSeg ? u.cA : u.cB) + j,
+          __stcg(p.part1 + ((size_t)(me - first) * pairs + r.g_pair[group][pos]) * (2 * p.f) +
+                     (c < kSeg ? u.cA : u.cB) + j,
                  part[i]);
       }
-      if (!last_to_arrive(p.sync + kTickets1 + tile * G + group, S, &r)) continue;
+      if (!last_to_arrive(p.sync + kTickets1 + first, parts, &r)) continue;
       for (int i = tid; i < u.n * kSeg; i += kT) {
         const int pos = i / kSeg, j = i % kSeg;
         if (j >= u.wA) continue;
         const int q = r.g_pair[group][pos];
-        const float* at = p.part1 + (size_t)q * (2 * p.f) + u.cA + j;
+        const float* from = p.part1 + (size_t)q * (2 * p.f) + u.cA + j;
         const size_t step = (size_t)pairs * (2 * p.f);
-        float a[kMaxSplits], b[kMaxSplits];
-#pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s) {
-          a[s] = s < S ? __ldcg(at + s * step) : 0.f;
-          b[s] = s < S ? __ldcg(at + s * step + p.f) : 0.f;
-        }
         float ga = 0.f, up = 0.f;
+        for (int part0 = 0; part0 < parts; part0 += 4) {
+          float a[4], b[4];
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s) {
-          ga += a[s];
-          up += b[s];
+          for (int s = 0; s < 4; ++s) {
+            a[s] = part0 + s < parts ? __ldcg(from + (part0 + s) * step) : 0.f;
+            b[s] = part0 + s < parts ? __ldcg(from + (part0 + s) * step + p.f) : 0.f;
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            ga += a[s];
+            up += b[s];
+          }
         }
         put_h<F>(p, q, u.cA + j, ga, up, lane);
       }
@@ -759,12 +879,18 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
 
   // ------------------------------------------------------------------ down
   const int tiles = (p.d + kCols - 1) / kCols;
-  const int S = splits_for(G * tiles, (p.f + kStep * kWarps - 1) / (kStep * kWarps), p.cap2);
+  const Line line(G * tiles, (p.f + kStep - 1) / kStep, gridDim.x);
+  const int me = blockIdx.x;
+  long long at = me < line.ctas ? line.begin(me) : 0;
+  const long long stop = me < line.ctas ? line.begin(me + 1) : 0;
   const size_t expert_bytes = row_bytes_of<F>(p.d) * p.f;
-  auto make_unit = [&](int w, int* group, int* split, int* tile) {
+  // this CTA's part of the unit at step `at`
+  auto make_unit = [&](int* group, int* tile, int* s0, int* s1) {
+    const int w = line.unit(at);
     *group = w % G;
-    *split = w / G % S;
-    *tile = w / G / S;
+    *tile = w / G;
+    *s0 = (int)(at - (long long)w * line.steps);
+    *s1 = (int)min((long long)line.steps, *s0 + (stop - at));
     const int e = r.g_expert[*group];
     Unit u;
     u.W = p.dn + (size_t)e * expert_bytes;
@@ -776,48 +902,70 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
     u.wA = min(kSeg, p.d - u.cA);
     u.wB = max(0, min(kSeg, p.d - u.cB));
     u.n = r.g_n[*group];
-    split_rows(p.f, kStep, S, *split, &u.k0, &u.k1);
+    u.k0 = *s0 * kStep;
+    u.k1 = min(p.f, *s1 * kStep);
     return u;
   };
-  if ((int)blockIdx.x < G * tiles * S) {
-    // the first unit's rows on their way to L2 while the grid assembles
-    int group, split, tile;
-    const Unit u = make_unit(blockIdx.x, &group, &split, &tile);
+  int group, tile, s0, s1;
+  if (at < stop) {
+    // the first rows on their way to L2 while the grid assembles
+    const Unit u = make_unit(&group, &tile, &s0, &s1);
     const size_t row = row_bytes_of<F>(p.d);
     const size_t c0 = row_bytes_of<F>(u.cA), width = row_bytes_of<F>(u.wA + u.wB);
     const int lines = (int)((width + 127) / 128);
     for (int i = tid; i < (u.k1 - u.k0) * lines; i += kT) {
-      const uint8_t* at = u.W + (size_t)(u.k0 + i / lines) * row + c0 + min((size_t)(i % lines) * 128, width - 1);
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+      const uint8_t* from = u.W + (size_t)(u.k0 + i / lines) * row + c0 + min((size_t)(i % lines) * 128, width - 1);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
     }
   }
   if (!grid_barrier(p.sync + kSyncB, &r, p)) return;
-  for (int w = blockIdx.x; w < G * tiles * S; w += gridDim.x) {
-    int group, split, tile;
-    const Unit u = make_unit(w, &group, &split, &tile);
+  while (at < stop) {
+    const Unit u = make_unit(&group, &tile, &s0, &s1);
     unit_product<F, true>(p, &r, group, u, smem);
+    const long long unit_at = at - s0;
+    at += s1 - s0;
+    const int first = line.owner(unit_at);
     for (int i = tid; i < u.n * kCols; i += kT) {
       const int pos = i / kCols, c = i % kCols;
       if (u.cA + c < p.d)
-        __stcg(p.part2 + ((size_t)split * pairs + r.g_pair[group][pos]) * p.d + u.cA + c, part[i]);
+        __stcg(p.part2 + ((size_t)(me - first) * pairs + r.g_pair[group][pos]) * p.d + u.cA + c, part[i]);
     }
-    if (!last_to_arrive(p.sync + kTickets2 + tile, (unsigned)(G * S), &r)) continue;
+    // once per tile: after this CTA's last unit of it
+    const long long tile_at = (long long)tile * G * line.steps, tile_end = tile_at + (long long)G * line.steps;
+    if (at < stop && at < tile_end) continue;
+    const unsigned arrivals = (unsigned)(line.owner(tile_end - 1) - line.owner(tile_at) + 1);
+    if (!last_to_arrive(p.sync + kTickets2 + tile, arrivals, &r)) continue;
+    for (int g = tid; g < G; g += kT) {
+      const long long from = tile_at + (long long)g * line.steps;
+      const short parts = (short)(line.owner(from + line.steps - 1) - line.owner(from) + 1);
+      for (int i = 0; i < r.g_n[g]; ++i) r.parts[r.g_pair[g][i]] = parts;
+    }
+    __syncthreads();
     const int width = min(kCols, p.d - u.cA);
     for (int i = tid; i < p.M * width; i += kT) {
       const int m = i / width, c = u.cA + i % width;
       float y = 0.f;
-      for (int s0 = 0; s0 < p.k; ++s0) {
-        const float* at = p.part2 + (size_t)(m * p.k + s0) * p.d + c;
-        float v[kMaxSplits];
+      // eight experts' first two parts in flight; further parts are rare
+      for (int q0 = m * p.k; q0 < (m + 1) * p.k; q0 += 8) {
+        const int n = min(8, (m + 1) * p.k - q0);
+        float v[8][2];
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s) v[s] = s < S ? __ldcg(at + (size_t)s * pairs * p.d) : 0.f;
-        float sum = 0.f;
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s) sum += v[s];
-        y = fmaf(r.gate[m * p.k + s0], sum, y);
+          for (int s = 0; s < 2; ++s)
+            v[i][s] = i < n && s < r.parts[q0 + i]
+                          ? __ldcg(p.part2 + ((size_t)s * pairs + q0 + i) * p.d + c) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= n) break;
+          float sum = v[i][0] + v[i][1];
+          for (int s = 2; s < r.parts[q0 + i]; ++s) sum += __ldcg(p.part2 + ((size_t)s * pairs + q0 + i) * p.d + c);
+          y = fmaf(r.gate[q0 + i], sum, y);
+        }
       }
       p.y[(size_t)m * p.d + c] = y;
     }
+    __syncthreads();  // r.parts is read
   }
 
   // the barriers' words are zero again once every CTA has passed both
@@ -831,24 +979,19 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
 
 int seg_of(MoeFormat f) { return f == MoeFormat::MX4 ? 128 : 64; }
 
-// Most splits a phase can use: there are at least k groups (a token's experts
-// differ) and one for every eight pairs.
-int split_cap(int M, int k, int tiles, int grid) {
-  const int groups = std::max(k, (M * k + kGroup - 1) / kGroup);
-  return std::max(1, std::min(kMaxSplits, grid / std::max(1, groups * tiles)));
-}
-
 struct MoePlan {
-  int cap1, cap2;
   size_t logits, xop, hop, part1, part2, total;
 };
 
 MoePlan make_plan(int M, int d, int f, int E, int k, MoeFormat fmt) {
   MoePlan pl;
-  const int seg = seg_of(fmt);
+  const int seg = seg_of(fmt), step = fmt == MoeFormat::BF16 ? 16 : 32;
   const int grid = 148 * kCtasPerSm;
-  pl.cap1 = split_cap(M, k, (f + seg - 1) / seg, grid);
-  pl.cap2 = split_cap(M, k, (d + 2 * seg - 1) / (2 * seg), grid);
+  // A unit spans the most CTAs where there are the fewest units: there are at
+  // least k groups (a token's experts differ) and one for every eight pairs.
+  const int groups = std::max(k, (M * k + kGroup - 1) / kGroup);
+  const int parts1 = Line(groups * ((f + seg - 1) / seg), (d + step - 1) / step, grid).parts();
+  const int parts2 = Line(groups * ((d + 2 * seg - 1) / (2 * seg)), (f + step - 1) / step, grid).parts();
   const size_t pairs = (size_t)M * k;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -859,8 +1002,8 @@ MoePlan make_plan(int M, int d, int f, int E, int k, MoeFormat fmt) {
   pl.logits = take((size_t)M * E * 8);
   pl.xop = take(fmt == MoeFormat::MX4 ? (size_t)M * d * 4 + (size_t)M * (d / 32) * 4 : 0);
   pl.hop = take(pairs * f * (fmt == MoeFormat::BF16 ? 6 : 4) + pairs * (f / 32 + 1) * 4);
-  pl.part1 = take(pl.cap1 > 1 ? (size_t)pl.cap1 * pairs * 2 * f * 4 : 0);
-  pl.part2 = take((size_t)pl.cap2 * pairs * d * 4);
+  pl.part1 = take((size_t)parts1 * pairs * 2 * f * 4);
+  pl.part2 = take((size_t)parts2 * pairs * d * 4);
   pl.total = off;
   return pl;
 }
@@ -882,7 +1025,7 @@ cudaError_t launch_fmt(const MParams& p, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, moe_kernel<F>, kT, Cfg<F>::kSmem);
     if (e != cudaSuccess) return e;
     if (per < 1) return cudaErrorLaunchOutOfResources;
-    // at most the grid that the split caps were made for
+    // at most the grid that the workspace is laid out for
     grids[dev] = std::min(std::min(per, kCtasPerSm) * sms, kCtasPerSm * 148);
   }
   cudaLaunchConfig_t cfg = {};
@@ -934,8 +1077,6 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
   p.f = a.f;
   p.E = a.E;
   p.k = a.k;
-  p.cap1 = pl.cap1;
-  p.cap2 = pl.cap2;
   p.renormalize = a.renormalize ? 1 : 0;
   p.x_f32 = a.x_elem == Elem::F32 ? 1 : 0;
   p.dev_status = a.dev_status;
