@@ -3,6 +3,11 @@
 // arithmetic.  A warp multiplies blocks of 32 rows by 128 columns; lane
 // (g, t) = (lane / 4, lane % 4) holds the columns 16 g .. 16 g + 15 of the
 // rows 4 t .. 4 t + 3 of a 16-row step.
+//
+// Two layouts of the eight columns of a B operand: up to four tokens, column
+// 2 token + piece (both pieces in one MMA); more tokens, eight tokens of one
+// piece, an MMA per piece, so that a lane's two accumulator columns are two
+// tokens and the scaling runs on pairs (fma.rn.f32x2).
 #pragma once
 
 #include "mx4.cuh"
@@ -151,14 +156,125 @@ __device__ __forceinline__ void block_product(const RowSet& rs, const uint2 (&b)
   }
 }
 
-// The B operands of up to 4 nt tokens over all their blocks, in global memory:
-// pieces [block][step][token / 4][2 (token % 4) + piece][16] f16, scales
-// [block][4 nt], and a word per block and token of which rows are not zero.
+// ---------------------------------------------------------------- eight tokens per operand
+
+__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Column pair q: see block_product8.
+template <int O, int q>
+__device__ __forceinline__ void column_pair8(const uint32_t (&w)[2][4], uint32_t scales, const uint2 (&b)[2][O][2],
+                                             const unsigned long long (&sx)[O], unsigned long long (&acc)[O][16],
+                                             int at) {
+  const uint32_t a[2][4] = {
+      {e2m1_to_f16<q>(w[0][0]), e2m1_to_f16<q>(w[0][1]), e2m1_to_f16<q>(w[0][2]), e2m1_to_f16<q>(w[0][3])},
+      {e2m1_to_f16<q>(w[1][0]), e2m1_to_f16<q>(w[1][1]), e2m1_to_f16<q>(w[1][2]), e2m1_to_f16<q>(w[1][3])}};
+  float s0, s1;
+  scale_pair(q & 1 ? scales >> 16 : scales & 0xffffu, &s0, &s1);
+  const unsigned long long ss0 = pack2(s0, s0), ss1 = pack2(s1, s1), low = pack2(0x1p-11f, 0x1p-11f);
+#pragma unroll
+  for (int o = 0; o < O; ++o) {
+    float d0[4], d1[4];
+    mma_f16(d0, true, a[0][0], a[0][1], a[0][2], a[0][3], b[0][o][0]);
+    mma_f16(d1, true, a[0][0], a[0][1], a[0][2], a[0][3], b[0][o][1]);
+    mma_f16(d0, false, a[1][0], a[1][1], a[1][2], a[1][3], b[1][o][0]);
+    mma_f16(d1, false, a[1][0], a[1][1], a[1][2], a[1][3], b[1][o][1]);
+    const unsigned long long v0 = fma2(pack2(d1[0], d1[1]), low, pack2(d0[0], d0[1]));
+    const unsigned long long v1 = fma2(pack2(d1[2], d1[3]), low, pack2(d0[2], d0[3]));
+    acc[o][at] = fma2(mul2(v0, sx[o]), ss0, acc[o][at]);
+    acc[o][at + 1] = fma2(mul2(v1, sx[o]), ss1, acc[o][at + 1]);
+  }
+}
+
+// acc[o][c] += (block product of the tokens 8 o + 2 t and 8 o + 2 t + 1 and
+// column c of the lane's 16), all 32 rows.  b[step][o][piece]: B operands;
+// sx[o]: the two tokens' scales.
+template <int O>
+__device__ __forceinline__ void block_product8(const RowSet& rs, const uint2 (&b)[2][O][2],
+                                               const unsigned long long (&sx)[O], unsigned long long (&acc)[O][16]) {
+  const uint32_t sw[4] = {rs.s.x, rs.s.y, rs.s.z, rs.s.w};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t w[2][4];
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = half == 0 ? rs.w[step][i].x : rs.w[step][i].y;
+      pair_rows(r[0], r[1], &w[step][0], &w[step][1]);
+      pair_rows(r[2], r[3], &w[step][2], &w[step][3]);
+    }
+    column_pair8<O, 0>(w, sw[2 * half], b, sx, acc, 8 * half);
+    column_pair8<O, 1>(w, sw[2 * half], b, sx, acc, 8 * half + 2);
+    column_pair8<O, 2>(w, sw[2 * half + 1], b, sx, acc, 8 * half + 4);
+    column_pair8<O, 3>(w, sw[2 * half + 1], b, sx, acc, 8 * half + 6);
+  }
+}
+
+// ---------------------------------------------------------------- copies of whole blocks
+
+// A warp's copies of 32-row blocks `stride` blocks apart, 128 columns each,
+// into a ring of tiles.  A lane brings 16 bytes of four rows (tile positions
+// lane / 4 + 8 j), the first eight lanes also 16 scale bytes.
+struct BlockCopies {
+  const uint8_t* rows;    // this lane's bytes of the next block's first row
+  const uint8_t* scales;  // and of its scales
+  size_t row_step, scale_step;
+  uint32_t off[4];
+
+  // Columns [c0, c0 + width) of a matrix of ld columns from block `block` on;
+  // columns past the width name the last ones.
+  __device__ __forceinline__ void start(const uint8_t* codes, const uint8_t* all_scales, int ld, int c0, int width,
+                                        int block, int stride, int lane) {
+    const uint32_t row_bytes = (uint32_t)ld / 2;
+    rows = codes + (size_t)block * kBlock * row_bytes + c0 / 2 + min(16 * (lane & 3), width / 2 - 16);
+    scales = all_scales + (size_t)block * ld + c0 + min(16 * lane, width - 16);
+    row_step = (size_t)stride * kBlock * row_bytes;
+    scale_step = (size_t)stride * ld;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) off[j] = row_of(8 * j + (lane >> 2)) * row_bytes;
+  }
+  // Row of the block at a tile position.
+  static __device__ __forceinline__ uint32_t row_of(int pos) {
+    return (uint32_t)((pos & 16) + (pos & 3) * 4 + ((pos >> 2) & 3));
+  }
+  // Copies the next block and moves on; commits a group.
+  __device__ __forceinline__ void next(Tile& tile, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) copy16_l2(&tile.row[8 * j + (lane >> 2)][16 * (lane & 3)], rows + off[j]);
+    if (lane < 8) copy16_l2(&tile.scale[16 * lane], scales);
+    rows += row_step;
+    scales += scale_step;
+  }
+};
+
+// The B operands of up to 8 octets tokens over all their blocks, in global memory:
+// pieces [block][step][token / 8][piece][token % 8][16] f16, scales
+// [block][8 octets], and a word per block and token of which rows are not
+// zero.
 struct Operand {
   __half* piece = nullptr;
   float* sx = nullptr;
   unsigned* mask = nullptr;
-  int nt = 0;
+  int octets = 0;
 
   // Lane `lane` of a whole warp holds value v of row `lane` of a block of
   // token m; the warp writes its operand.
@@ -169,12 +285,12 @@ struct Operand {
     piece_scale(top, &up, &down);
     __half p0, p1;
     split_pieces(v * up, &p0, &p1);
-    __half* at = piece + ((((size_t)block * 2 + (lane >> 4)) * nt + (m >> 2)) * 8 + (m & 3) * 2) * 16 + (lane & 15);
+    __half* at = piece + ((((size_t)block * 2 + (lane >> 4)) * octets + (m >> 3)) * 16 + (m & 7)) * 16 + (lane & 15);
     at[0] = p0;
-    at[16] = p1;
+    at[128] = p1;
     if (lane == 0) {
-      sx[(size_t)block * 4 * nt + m] = down;
-      mask[(size_t)block * 4 * nt + m] = kept;
+      sx[(size_t)block * 8 * octets + m] = down;
+      mask[(size_t)block * 8 * octets + m] = kept;
     }
   }
 };

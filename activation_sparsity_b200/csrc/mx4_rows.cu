@@ -68,10 +68,8 @@ namespace {
 
 constexpr int kRThreads = 256;
 constexpr int kRWarps = kRThreads / 32;
-constexpr int kRing = 3;      // tiles of a warp's ring, 5 to 16 tokens
 constexpr int kFewRing = 3;   // up to 4 tokens
 constexpr int kFewCtas = 3;   // CTAs per SM, up to 4 tokens
-constexpr int kManyCtas = 2;  // 5 to 16 tokens
 constexpr int kMaxSplits = 16;
 constexpr int kMaxSplitRows = 16384;  // rows of one split a kept list is scattered into
 
@@ -90,31 +88,21 @@ struct RParams {
   int* dev_status;
 };
 
-// The CTA's sums of every warp, added in warp order, then those of the tile's
-// splits in split order, to y.  Warp w holds columns (w % kHalves) 128 ... of
-// the tile.
-template <int NT, int kHalves>
-__device__ __forceinline__ void reduce_tile(const float (&acc)[NT][8][2], float* part, const RParams& p) {
-  constexpr int kTok = 4 * NT;
+// Adds the CTA's sums part[block lane][token][column] in lane order, then
+// those of the tile's splits in split order, to y.
+template <int kTok, int kHalves, int kThreads = kRThreads>
+__device__ __forceinline__ void add_parts(float* part, const RParams& p) {
   constexpr int kCols = 128 * kHalves;
   __shared__ unsigned s_order;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  // [block lane][token][column]
-  float* mine = part + ((size_t)(warp / kHalves) * kTok + t) * kCols + (warp % kHalves) * 128 + g * 16;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<float2*>(mine + (size_t)4 * n * kCols + 2 * q) = make_float2(acc[n][q][0], acc[n][q][1]);
+  const int tid = threadIdx.x;
   __syncthreads();
   const int S = gridDim.x, tile = blockIdx.y, count = p.M * kCols;
   float* slab = p.partials + ((size_t)blockIdx.x * gridDim.y + tile) * count;
-  for (int e = tid; e < count / 4; e += kRThreads) {
+  for (int e = tid; e < count / 4; e += kThreads) {
     const float4* from = reinterpret_cast<const float4*>(part) + e;
     float4 s = *from;
 #pragma unroll
-    for (int w = 1; w < kRWarps / kHalves; ++w) {
+    for (int w = 1; w < kThreads / 32 / kHalves; ++w) {
       const float4 v = from[w * kTok * kCols / 4];
       s.x += v.x;
       s.y += v.y;
@@ -135,7 +123,7 @@ __device__ __forceinline__ void reduce_tile(const float (&acc)[NT][8][2], float*
   if (s_order != (unsigned)S - 1u) return;
   // four columns at a time, every split's in flight, added in split order
   const size_t step = (size_t)gridDim.y * count / 4;
-  for (int e = tid; e < count / 4; e += kRThreads) {
+  for (int e = tid; e < count / 4; e += kThreads) {
     const float4* from = reinterpret_cast<const float4*>(p.partials + (size_t)tile * count) + e;
     float4 v[kMaxSplits];
 #pragma unroll
@@ -357,42 +345,60 @@ __global__ void __launch_bounds__(kRThreads, kFewCtas) mx4_rows_few_kernel(const
     mx4::copies_wait<0>();
   }
   __syncthreads();
-  // lanes of tokens that do not exist hold whatever their columns held; only
-  // tokens below M are added
-  reduce_tile<1, kHalves>(acc, reinterpret_cast<float*>(smem), p);
+  // [block lane][token][column]; lanes of tokens that do not exist hold
+  // whatever their columns held, and only tokens below M are added
+  float* part = reinterpret_cast<float*>(smem);
+  float* mine = part + ((size_t)(warp / kHalves) * 4 + t) * (128 * kHalves) + (warp % kHalves) * 128 + g * 16;
+#pragma unroll
+  for (int q = 0; q < 8; q += 2)
+    *reinterpret_cast<float4*>(mine + 2 * q) =
+        make_float4(acc[0][q][0], acc[0][q][1], acc[0][q + 1][0], acc[0][q + 1][1]);
+  add_parts<4, kHalves>(part, p);
 }
 
 // ---------------------------------------------------------------- 5 to 16 tokens
 
-// A tile and its block's operand and token scales.
-template <int NT>
+// A tile and its block's operand and token scales, O octets of tokens.
+template <int O>
 struct __align__(16) ManyTile {
   mx4::Tile rows;
-  __half piece[2][NT][8][16];
-  float sx[4 * NT];
+  __half piece[2][O][2][8][16];
+  float sx[8 * O];
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kRThreads, kManyCtas) mx4_rows_many_kernel(const RParams p) {
+// Sixteen tokens' accumulators and operands take 168 registers: twelve warps
+// in one CTA per SM (with sixteen warps of 128 registers they spill).
+template <int O>
+struct ManyCfg {
+  static constexpr int kThreads = O == 1 ? 256 : 384;
+  static constexpr int kCtas = O == 1 ? 2 : 1;  // per SM
+  static constexpr int kRing = O == 1 ? 3 : 4;  // tiles of a warp's ring
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr size_t kBytes = sizeof(ManyTile<O>) * kRing * kWarps;
+  static_assert((size_t)(kWarps / 2) * 8 * O * 256 * 4 <= kBytes, "the sums reuse the rings");
+};
+
+template <int O>
+__global__ void __launch_bounds__(ManyCfg<O>::kThreads, ManyCfg<O>::kCtas) mx4_rows_many_kernel(const RParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int kTok = 4 * NT;
-  constexpr int kHalves = 2, kLanes = kRWarps / kHalves;
+  constexpr int kTok = 8 * O, kRing = ManyCfg<O>::kRing;
+  constexpr int kHalves = 2, kLanes = ManyCfg<O>::kWarps / kHalves;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  ManyTile<NT>* ring = reinterpret_cast<ManyTile<NT>*>(smem) + warp * kRing;
+  ManyTile<O>* ring = reinterpret_cast<ManyTile<O>*>(smem) + warp * kRing;
   const int n_blocks = p.d_in / mx4::kBlock;
   const int b_begin = blockIdx.x * p.blocks_per_split;
   const int b_end = min(n_blocks, b_begin + p.blocks_per_split);
   const int col0 = (int)blockIdx.y * 128 * kHalves + (warp % kHalves) * 128;
-  const uint32_t row_bytes = (uint32_t)p.d_out / 2;
-  const uint32_t chunk = min((uint32_t)col0 / 2 + 16u * (lane & 3), row_bytes - 16u);
-  const uint8_t* s_col = p.scales + min(col0 + 16 * lane, p.d_out - 16);
+  int b = b_begin + warp / kHalves;
+  mx4::BlockCopies copies;
+  copies.start(p.codes, p.scales, p.d_out, min(col0, p.d_out - 32), max(32, min(128, p.d_out - col0)), b, kLanes, lane);
 
-  float acc[NT][8][2];
+  unsigned long long acc[O][16];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int o = 0; o < O; ++o)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[n][q][0] = acc[n][q][1] = 0.f;
+    for (int c = 0; c < 16; ++c) acc[o][c] = 0ull;
 
   pdl_wait();
   pdl_launch_dependents();
@@ -402,25 +408,34 @@ __global__ void __launch_bounds__(kRThreads, kManyCtas) mx4_rows_many_kernel(con
     return b < b_end && lane < p.M ? __ldg(p.op.mask + (size_t)b * kTok + lane) : 0u;
   };
   auto any_token = [&](unsigned m) -> unsigned { return __reduce_or_sync(0xffffffffu, m); };
-  auto copy = [&](int b, unsigned kept, int stage_no) {
-    if (kept != 0u) {
-      ManyTile<NT>& tile = ring[stage_no];
-      const uint32_t first = (uint32_t)__ffs(kept) - 1u;
-      copy_tile(tile.rows, p.codes + (size_t)b * 32 * row_bytes, chunk, 32, s_col + (size_t)b * p.d_out, lane,
-                [&](int pos) {
-                  const uint32_t r = (pos & 16) + (pos & 3) * 4 + ((pos >> 2) & 3);
-                  return ((kept >> r) & 1u ? r : first) * row_bytes;
-                });
-      const unsigned char* src = reinterpret_cast<const unsigned char*>(p.op.piece) + (size_t)b * (512 * NT);
-      unsigned char* dst = reinterpret_cast<unsigned char*>(tile.piece);
+  int at = b;  // the block the copies have come to
+  auto copy = [&](unsigned kept, ManyTile<O>& tile) {
+    if (kept == ~0u) {
+      copies.next(tile.rows, lane);
+    } else if (at < b_end) {
+      // rows that no token keeps are replaced by the first that one does
+      mx4::BlockCopies some = copies;
+      const uint32_t first = kept ? (uint32_t)__ffs(kept) - 1u : 0u;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) mx4::copy16_l1(dst + 512 * i + 16 * lane, src + 512 * i + 16 * lane);
-      if (lane < NT) mx4::copy16_l1(&tile.sx[4 * lane], p.op.sx + (size_t)b * kTok + 4 * lane);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t row = mx4::BlockCopies::row_of(8 * j + (lane >> 2));
+        if (!((kept >> row) & 1u)) some.off[j] = first * ((uint32_t)p.d_out / 2);
+      }
+      if (kept != 0u) some.next(tile.rows, lane);
+      copies.rows += copies.row_step;
+      copies.scales += copies.scale_step;
     }
+    if (kept != 0u) {
+      const unsigned char* src = reinterpret_cast<const unsigned char*>(p.op.piece) + (size_t)at * (1024 * O) + 16 * lane;
+      unsigned char* dst = reinterpret_cast<unsigned char*>(tile.piece) + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < 2 * O; ++i) mx4::copy16_l1(dst + 512 * i, src + 512 * i);
+      if (lane < 2 * O) mx4::copy16_l1(&tile.sx[4 * lane], p.op.sx + (size_t)at * kTok + 4 * lane);
+    }
+    at += kLanes;
     mx4::copies_commit();
   };
 
-  int b = b_begin + warp / kHalves;
   // kept[s]: rows of the block in tile s of the ring, and of the one after;
   // masks are read two blocks before they are needed
   unsigned kept[kRing], raw[kRing];
@@ -430,35 +445,55 @@ __global__ void __launch_bounds__(kRThreads, kManyCtas) mx4_rows_many_kernel(con
 #pragma unroll
   for (int s = 0; s < kRing; ++s) kept[s] = any_token(raw[s]);
 #pragma unroll
-  for (int s = 0; s < kRing - 1; ++s) copy(b + s * kLanes, kept[s], s);
-  for (int it = 0; b < b_end; b += kLanes, ++it) {
+  for (int s = 0; s < kRing - 1; ++s) copy(kept[s], ring[s]);
+  int now = 0, fill = kRing - 1;
+  for (; b < b_end; b += kLanes) {
     __syncwarp();  // every lane has read the tile that is filled next
-    copy(b + (kRing - 1) * kLanes, kept[kRing - 1], (it + kRing - 1) % kRing);
+    copy(kept[kRing - 1], ring[fill]);
     const unsigned after = any_token(raw_next);
     raw_next = read_mask(b + (kRing + 1) * kLanes);
     mx4::copies_wait<kRing - 1>();
     __syncwarp();  // the other lanes' copies too
     if (kept[0] != 0u) {
-      const ManyTile<NT>& tile = ring[it % kRing];
+      const ManyTile<O>& tile = ring[now];
       mx4::RowSet rs;
       rs.read<4, 4>(tile.rows, g, t);
-      uint2 bop[2][NT];
-      float sx[NT];
+      uint2 bop[2][O][2];
+      unsigned long long sx[O];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int o = 0; o < O; ++o) {
 #pragma unroll
-        for (int step = 0; step < 2; ++step) bop[step][n] = *reinterpret_cast<const uint2*>(&tile.piece[step][n][g][4 * t]);
-        sx[n] = tile.sx[4 * n + t];
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece)
+            bop[step][o][piece] = *reinterpret_cast<const uint2*>(&tile.piece[step][o][piece][g][4 * t]);
+        sx[o] = *reinterpret_cast<const unsigned long long*>(&tile.sx[8 * o + 2 * t]);
       }
-      mx4::block_product<NT, 4, 4>(rs, bop, sx, acc);
+      mx4::block_product8<O>(rs, bop, sx, acc);
     }
+    now = now + 1 == kRing ? 0 : now + 1;
+    fill = fill + 1 == kRing ? 0 : fill + 1;
 #pragma unroll
     for (int s = 0; s < kRing - 1; ++s) kept[s] = kept[s + 1];
     kept[kRing - 1] = after;
   }
   mx4::copies_wait<0>();
   __syncthreads();
-  reduce_tile<NT, kHalves>(acc, reinterpret_cast<float*>(smem), p);
+  // [block lane][token][column]
+  float* part = reinterpret_cast<float*>(smem);
+  constexpr int kCols = 128 * kHalves;
+  float* mine = part + ((size_t)(warp / kHalves) * kTok + 2 * t) * kCols + (warp % kHalves) * 128 + g * 16;
+#pragma unroll
+  for (int o = 0; o < O; ++o)
+#pragma unroll
+    for (int c = 0; c < 16; c += 4) {
+      const float2 v[4] = {mx4::unpack2(acc[o][c]), mx4::unpack2(acc[o][c + 1]), mx4::unpack2(acc[o][c + 2]),
+                           mx4::unpack2(acc[o][c + 3])};
+      float* to = mine + (size_t)8 * o * kCols + c;
+      *reinterpret_cast<float4*>(to) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+      *reinterpret_cast<float4*>(to + kCols) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+    }
+  add_parts<kTok, kHalves, ManyCfg<O>::kThreads>(part, p);
 }
 
 // ---------------------------------------------------------------- kept lists to dense rows or operands
@@ -547,10 +582,10 @@ cudaError_t allow_smem(F* fn, size_t bytes, int (&done)[64]) {
 }
 
 template <typename F>
-cudaError_t launch_tiles(F* fn, RParams p, int halves, int slots, size_t smem, cudaStream_t stream) {
+cudaError_t launch_tiles(F* fn, RParams p, int halves, int warps, int slots, size_t smem, cudaStream_t stream) {
   const int tiles = (p.d_out + 128 * halves - 1) / (128 * halves);
   const int n_blocks = p.d_in / mx4::kBlock;
-  int S = pick_splits(tiles, n_blocks, kRWarps / halves, slots);
+  int S = pick_splits(tiles, n_blocks, warps / halves, slots);
   if (p.idx != nullptr) {  // the split's coefficients are staged in shared memory
     while (((n_blocks + S - 1) / S) * 32 > kMaxSplitRows) ++S;
     smem += (size_t)((n_blocks + S - 1) / S) * 32 * 4;
@@ -558,7 +593,7 @@ cudaError_t launch_tiles(F* fn, RParams p, int halves, int slots, size_t smem, c
   p.blocks_per_split = (n_blocks + S - 1) / S;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S, tiles, 1);
-  cfg.blockDim = dim3(kRThreads, 1, 1);
+  cfg.blockDim = dim3(32 * warps, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -576,7 +611,7 @@ cudaError_t launch_few(const RParams& p, cudaStream_t stream) {
   auto* fn = mx4_rows_few_kernel<kList, kM, kHalves>;
   const cudaError_t e = allow_smem(fn, kBytes + (kList ? (size_t)kMaxSplitRows * 4 : 0), done);
   if (e != cudaSuccess) return e;
-  return launch_tiles(fn, p, kHalves, kFewCtas * 148, kBytes, stream);
+  return launch_tiles(fn, p, kHalves, kRWarps, kFewCtas * 148, kBytes, stream);
 }
 
 // 256 columns per CTA where that still gives every SM its CTAs.
@@ -586,26 +621,25 @@ cudaError_t launch_few(const RParams& p, cudaStream_t stream) {
   return wide ? launch_few<kList, kM, 2>(p, stream) : launch_few<kList, kM, 1>(p, stream);
 }
 
-template <int NT>
+template <int O>
 cudaError_t launch_many(const RParams& p, cudaStream_t stream) {
-  constexpr size_t kBytes = sizeof(ManyTile<NT>) * kRing * kRWarps;
-  static_assert((size_t)(kRWarps / 2) * 4 * NT * 256 * 4 <= kBytes, "the sums reuse the rings");
+  using C = ManyCfg<O>;
   static int done[64] = {0};
-  cudaError_t e = allow_smem(mx4_rows_many_kernel<NT>, kBytes, done);
+  cudaError_t e = allow_smem(mx4_rows_many_kernel<O>, C::kBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_tiles(mx4_rows_many_kernel<NT>, p, 2, kManyCtas * 148, kBytes, stream);
+  return launch_tiles(mx4_rows_many_kernel<O>, p, 2, C::kWarps, C::kCtas * 148, C::kBytes, stream);
 }
 
-// Token groups of four an operand is laid out for (1 to 4 tokens use none).
-int groups_of(int M) { return M <= 8 ? 2 : 4; }
+// Octets of tokens an operand is laid out for (1 to 4 tokens use none).
+int octets_of(int M) { return (M + 7) / 8; }
 
 mx4::Operand operand_at(void* buf, int M, int d_in) {
   mx4::Operand op;
-  op.nt = groups_of(M);
+  op.octets = octets_of(M);
   const size_t blocks = (size_t)d_in / mx4::kBlock;
   op.piece = static_cast<__half*>(buf);
-  op.sx = reinterpret_cast<float*>(op.piece + blocks * 256 * op.nt);
-  op.mask = reinterpret_cast<unsigned*>(op.sx + blocks * 4 * op.nt);
+  op.sx = reinterpret_cast<float*>(op.piece + blocks * 512 * op.octets);
+  op.mask = reinterpret_cast<unsigned*>(op.sx + blocks * 8 * op.octets);
   return op;
 }
 
@@ -618,7 +652,7 @@ namespace {
 // sums follow.
 size_t coef_bytes(int M, int d_in) {
   const size_t blocks = (size_t)d_in / mx4::kBlock;
-  const size_t n = mx4_rows_take_operand(M) ? blocks * groups_of(M) * (512 + 4 * 4 + 4 * 4) : (size_t)M * d_in * 4;
+  const size_t n = mx4_rows_take_operand(M) ? blocks * octets_of(M) * (1024 + 8 * 4 + 8 * 4) : (size_t)M * d_in * 4;
   return (n + 255) / 256 * 256;
 }
 }  // namespace
@@ -674,7 +708,7 @@ cudaError_t launch_mx4_rows(const int32_t* idx, const float* val, int K, void* b
     return M == 1 ? launch_few<false, 1>(p, stream) : launch_few<false, 4>(p, stream);
   }
   p.op = operand_at(buf, M, d_in);
-  return M <= 8 ? launch_many<2>(p, stream) : launch_many<4>(p, stream);
+  return M <= 8 ? launch_many<1>(p, stream) : launch_many<2>(p, stream);
 }
 
 }  // namespace larosa
