@@ -418,9 +418,10 @@ template <>
 struct Cfg<Fmt::MX4> {
   static constexpr int kSeg = 128;
   static constexpr int kStep = 32;
-  static constexpr int kRing = 2;
-  static constexpr size_t kSmem = (size_t)kWarps * kRing * 2 * sizeof(mx4::Tile);
-  static_assert(kSmem >= (size_t)kWarps * kGroup * 2 * kSeg * 4, "the sums reuse the rings");
+  static constexpr int kRing = 3;  // tiles of a warp's ring
+  static constexpr size_t kRingBytes = (size_t)kWarps * kRing * sizeof(mx4::Tile);
+  static constexpr size_t kPart = (size_t)kWarps * kGroup * kSeg * 4;  // a segment's sums of every warp
+  static constexpr size_t kSmem = kRingBytes + kPart + (size_t)kGroup * 2 * kSeg * 4;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
@@ -540,83 +541,131 @@ __device__ __forceinline__ void product_f32(const Unit& u, const float* const (&
         make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
 }
 
-// MX4 weights: blocks of 32 rows, both segments of a block through the warp's
-// ring of tiles.  op[n], sx[n]: pieces (this lane's column: token 4 n + g / 2,
-// piece g % 2) and block scales of token 4 n + t (null: no token).
-template <int NT>
-__device__ __forceinline__ void product_mx4(const Unit& u, const __half* const (&op)[NT], const float* const (&sx)[NT],
+// MX4 weights: blocks of 32 rows by 128 columns through the warp's ring of
+// tiles, segment A's, then B's, in one stream; after a segment the warps' sums
+// are added, in warp order, into sums[token][256].
+//   kEight   op: pieces of the token in column g of B (token g), the second
+//            `rows` halves after the first; sx: block scales of the tokens 2 t
+//            and 2 t + 1
+//   else     up to four tokens; op: piece g % 2 of token g / 2; sx[0]: of token t
+// Null: no token.
+template <bool kEight>
+__device__ __forceinline__ void product_mx4(const Unit& u, const __half* op, const float* const (&sx)[2],
                                             unsigned char* smem) {
-  constexpr int kRing = Cfg<Fmt::MX4>::kRing;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using C = Cfg<Fmt::MX4>;
+  constexpr int kRing = C::kRing;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  mx4::Tile(*ring)[2] = reinterpret_cast<mx4::Tile(*)[2]>(smem) + warp * kRing;
-  const uint32_t row_bytes = (uint32_t)u.ld / 2;
-  float acc[2][NT][8][2] = {};
-  const int b0 = u.k0 / 32, b1 = u.k1 / 32;
-  auto copy = [&](int b, int s) {
-    if (b < b1) {
-#pragma unroll
-      for (int seg = 0; seg < 2; ++seg) {
-        const int c0 = seg == 0 ? u.cA : u.cB, w = seg == 0 ? u.wA : u.wB;
-        if (w > 0) {
-          mx4::Tile& tile = ring[s][seg];
-          // columns past the segment name its last ones
-          const uint32_t chunk = (uint32_t)c0 / 2 + min(16u * (lane & 3), (uint32_t)w / 2 - 16u);
-          const uint8_t* from = u.W + (size_t)b * 32 * row_bytes + chunk;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int pos = 8 * j + (lane >> 2);
-            const uint32_t row = (pos & 16) + (pos & 3) * 4 + ((pos >> 2) & 3);
-            mx4::copy16_l2(&tile.row[pos][16 * (lane & 3)], from + row * row_bytes);
-          }
-          if (lane < 8)
-            mx4::copy16_l2(&tile.scale[16 * lane], u.scales + (size_t)b * u.ld + c0 + min(16 * lane, w - 16));
-        }
-      }
+  mx4::Tile* ring = reinterpret_cast<mx4::Tile*>(smem) + warp * kRing;
+  float* part = reinterpret_cast<float*>(smem + C::kRingBytes);
+  float* sums = reinterpret_cast<float*>(smem + C::kRingBytes + C::kPart);
+  const int first = u.k0 / 32 + warp, last = u.k1 / 32;
+  const int mine = first < last ? (last - first + kWarps - 1) / kWarps : 0;  // this warp's blocks
+  const int segs = u.wB > 0 ? 2 : 1;
+
+  mx4::BlockCopies copies;
+  copies.start(u.W, u.scales, u.ld, u.cA, u.wA, first, kWarps, lane);
+  int issued = 0, fill = 0;
+  auto issue = [&]() {
+    if (issued < mine * segs) {
+      if (issued == mine) copies.start(u.W, u.scales, u.ld, u.cB, u.wB, first, kWarps, lane);
+      copies.next(ring[fill], lane);
     }
+    ++issued;
+    fill = fill + 1 == kRing ? 0 : fill + 1;
     mx4::copies_commit();
   };
-  int b = b0 + warp;
+  struct Ops {
+    uint2 b[2][2];  // [step][piece]; up to four tokens: [step][0]
+    float s[2];
+  };
+  auto load_ops = [&](int i, Ops& o) {
+    const int b = first + i * kWarps;
 #pragma unroll
-  for (int s = 0; s < kRing - 1; ++s) copy(b + s * kWarps, s);
-  for (int it = 0; b < b1; b += kWarps, ++it) {
-    uint2 bop[2][NT];
-    float s[NT];
+    for (int step = 0; step < 2; ++step)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+      for (int piece = 0; piece < (kEight ? 2 : 1); ++piece)
+        o.b[step][piece] = op != nullptr && i < mine ? *reinterpret_cast<const uint2*>(
+                                                            op + (size_t)piece * u.rows + b * 32 + 16 * step + 4 * t)
+                                                     : make_uint2(0u, 0u);
 #pragma unroll
-      for (int step = 0; step < 2; ++step)
-        bop[step][n] = op[n] != nullptr ? *reinterpret_cast<const uint2*>(op[n] + b * 32 + 16 * step + 4 * t)
-                                        : make_uint2(0u, 0u);
-      s[n] = sx[n] != nullptr ? sx[n][b] : 0.f;
+    for (int i2 = 0; i2 < (kEight ? 2 : 1); ++i2) o.s[i2] = sx[i2] != nullptr && i < mine ? sx[i2][b] : 0.f;
+  };
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) issue();
+  int now = 0;
+  for (int seg = 0; seg < segs; ++seg) {
+    unsigned long long acc8[1][16];
+    float acc4[1][8][2];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      acc8[0][c] = 0ull;
+      acc4[0][c / 2][c % 2] = 0.f;
     }
-    __syncwarp();  // every lane has read the tiles that are filled next
-    copy(b + (kRing - 1) * kWarps, (it + kRing - 1) % kRing);
-    mx4::copies_wait<kRing - 1>();
-    __syncwarp();  // the other lanes' copies too
-#pragma unroll
-    for (int seg = 0; seg < 2; ++seg) {
-      if ((seg == 0 ? u.wA : u.wB) <= 0) continue;
+    Ops cur;
+    load_ops(0, cur);
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      __syncwarp();  // every lane has read the tile that is filled next
+      issue();
+      Ops next;
+      load_ops(i + 1, next);
+      mx4::copies_wait<kRing - 1>();
+      __syncwarp();  // the other lanes' copies too
       mx4::RowSet rs;
-      rs.read<4, 4>(ring[it % kRing][seg], g, t);
-      mx4::block_product<NT, 4, 4>(rs, bop, s, acc[seg]);
+      rs.read<4, 4>(ring[now], g, t);
+      now = now + 1 == kRing ? 0 : now + 1;
+      if constexpr (kEight) {
+        const uint2 b[2][1][2] = {{{cur.b[0][0], cur.b[0][1]}}, {{cur.b[1][0], cur.b[1][1]}}};
+        const unsigned long long s2[1] = {mx4::pack2(cur.s[0], cur.s[1])};
+        mx4::block_product8<1>(rs, b, s2, acc8);
+      } else {
+        const uint2 b[2][1] = {{cur.b[0][0]}, {cur.b[1][0]}};
+        const float s1[1] = {cur.s[0]};
+        mx4::block_product<1, 4, 4>(rs, b, s1, acc4);
+      }
+      cur = next;
     }
+    // [warp][token][column]
+    if constexpr (kEight) {
+      float* at = part + ((size_t)warp * kGroup + 2 * t) * C::kSeg + 16 * g;
+#pragma unroll
+      for (int c = 0; c < 16; c += 4) {
+        const float2 v[4] = {mx4::unpack2(acc8[0][c]), mx4::unpack2(acc8[0][c + 1]), mx4::unpack2(acc8[0][c + 2]),
+                             mx4::unpack2(acc8[0][c + 3])};
+        *reinterpret_cast<float4*>(at + c) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
+        *reinterpret_cast<float4*>(at + C::kSeg + c) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+      }
+    } else {
+      float* at = part + ((size_t)warp * kGroup + t) * C::kSeg + 16 * g;
+#pragma unroll
+      for (int q = 0; q < 8; q += 2)
+        *reinterpret_cast<float4*>(at + 2 * q) =
+            make_float4(acc4[0][q][0], acc4[0][q][1], acc4[0][q + 1][0], acc4[0][q + 1][1]);
+    }
+    __syncthreads();
+    for (int e = tid; e < u.n * C::kSeg; e += kT) {
+      float s = part[e];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) s += part[(size_t)w * kGroup * C::kSeg + e];
+      sums[(e / C::kSeg) * 2 * C::kSeg + seg * C::kSeg + e % C::kSeg] = s;
+    }
+    __syncthreads();
   }
   mx4::copies_wait<0>();
-  __syncthreads();
-  float* part = reinterpret_cast<float*>(smem);  // [warp][token][256]
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int seg = 0; seg < 2; ++seg)
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<float2*>(part + ((size_t)warp * kGroup + 4 * n + t) * 256 + 128 * seg + 16 * g + 2 * q) =
-            make_float2(acc[seg][n][q][0], acc[seg][n][q][1]);
 }
 
-// The unit's sums over the CTA's warps end up in part[warp 0][token][column].
-// op of a pair: x's (phase 1: token q / k) or h's (phase 2: pair q) operand.
+// Where the unit's sums over the CTA's warps lie: [token][2 kSeg].
+template <Fmt F>
+__device__ __forceinline__ float* unit_sums(unsigned char* smem) {
+  if constexpr (F == Fmt::MX4)
+    return reinterpret_cast<float*>(smem + Cfg<F>::kRingBytes + Cfg<F>::kPart);
+  else
+    return reinterpret_cast<float*>(smem);
+}
+
+// The unit's sums.  Operand of a pair: x's (gate | up: token q / k) or h's
+// (down: pair q).
 template <Fmt F, bool kDown>
 __device__ void unit_product(const MParams& p, const Routing* r, int group, const Unit& u, unsigned char* smem) {
   constexpr int kCols = 2 * Cfg<F>::kSeg;
@@ -658,22 +707,20 @@ __device__ void unit_product(const MParams& p, const Routing* r, int group, cons
     const unsigned char* src = kDown ? p.hop : p.xop;
     const __half* pieces = reinterpret_cast<const __half*>(src);
     const float* scales = reinterpret_cast<const float*>(src + (size_t)(kDown ? p.M * p.k : p.M) * 4 * rows);
-    auto run = [&](auto nt) {
-      constexpr int NT = decltype(nt)::value;
-      const __half* op[NT];
-      const float* sx[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int a = operand(4 * n + (g >> 1)), b = operand(4 * n + t);
-        op[n] = a < 0 ? nullptr : pieces + ((size_t)a * 2 + (g & 1)) * rows;
-        sx[n] = b < 0 ? nullptr : scales + (size_t)b * (rows / 32);
-      }
-      product_mx4<NT>(u, op, sx, smem);
+    auto scales_of = [&](int pos) -> const float* {
+      const int o = operand(pos);
+      return o < 0 ? nullptr : scales + (size_t)o * (rows / 32);
     };
-    if (u.n <= 4)
-      run(std::integral_constant<int, 1>{});
-    else
-      run(std::integral_constant<int, 2>{});
+    if (u.n <= 4) {
+      const int o = operand(g >> 1);
+      const float* const sx[2] = {scales_of(t), nullptr};
+      product_mx4<false>(u, o < 0 ? nullptr : pieces + ((size_t)o * 2 + (g & 1)) * rows, sx, smem);
+    } else {
+      const int o = operand(g);
+      const float* const sx[2] = {scales_of(2 * t), scales_of(2 * t + 1)};
+      product_mx4<true>(u, o < 0 ? nullptr : pieces + (size_t)o * 2 * rows, sx, smem);
+    }
+    return;  // added up already
   }
   __syncthreads();
   for (int e = tid; e < u.n * kCols; e += kT) {
@@ -807,7 +854,7 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   const int G = r.groups;
 
   // ------------------------------------------------------------------ gate | up
-  float* part = reinterpret_cast<float*>(smem);
+  const float* part = unit_sums<F>(smem);
   {
     const int tiles = (p.f + kSeg - 1) / kSeg;
     const Line line(G * tiles, (p.d + kStep - 1) / kStep, gridDim.x);
