@@ -11,29 +11,30 @@
 // blocks down the rows.
 //
 // Few tokens make it a stream of the chosen experts' weights, bound by HBM
-// (bf16: one product per 2 bytes and token), in three phases that depend on
-// one another: scores, then gate|up, then down.  As three launches the two
-// boundaries cost a drain, a launch and a ramp each, more than the whole
-// stream of a small layer; here one cooperative grid passes two grid-wide
-// barriers, and a CTA asks for its first down rows to be brought into L2
-// before it waits at the second.
+// (bf16: one product per 2 bytes and token), in three steps that depend on one
+// another: scores, then gate|up, then down.  As launches of their own the
+// boundaries cost a drain, a launch and a ramp each, more than the whole stream
+// of a small layer; here one cooperative grid passes four grid-wide barriers
+// of about 1.2 us, and a warp asks for its first down rows to be brought into
+// L2 before it waits.
 //
 //   scores   a CTA per expert and four tokens, its warps each a share of the
 //            inputs, summed in fp64: selection is a comparison, so scores that
 //            differ by less than fp32 rounding must not swap.  (Products of
 //            two fp32 values are exact in fp64.)
 //   routing  every CTA makes the same selection and the same work list from
-//            the scores.  A group is an expert and up to eight of its tokens.
-//   products a unit is a group and a tile of columns (gate and up halves side
-//            by side).  The rows of all units, in order, are one line of warp
-//            steps that is cut into equal shares, one per CTA: the number of
-//            units follows from the routing (5 tokens of 60 experts made 396
-//            units for 296 CTAs: whole units would take twice the time of
-//            equal shares).  A CTA's eight warps take steps in turn and add
-//            their sums in warp order in shared memory; where a unit (down: a
-//            column tile) spans CTAs, their sums go through the workspace and
-//            the last to arrive adds them in a fixed order, so results repeat
-//            bit for bit.
+//            the scores.  A group is an expert and up to eight of its tokens;
+//            a unit is a group and 128 columns (gate|up of bf16 and fp32: 64
+//            gate columns and the 64 up columns beside them).
+//   products the row steps of all units, in order, are one line that is cut
+//            into equal shares, one per warp of the grid: how many units there
+//            are is known only after the routing (5 tokens of 60 experts made
+//            396 units for 296 CTAs), and a share is one long stream of rows
+//            with no barrier in it.  A warp writes the sums of its part of a
+//            unit to the workspace;
+//   joins    after a barrier, the parts of every sum are added in the order of
+//            the line: h from gate and up, then y from the experts.  Results
+//            repeat bit for bit.
 //
 // The products run on mma.sync.m16n8k16 with fp32 accumulators: eight tokens
 // of fp32 FMAs per 2-byte weight would be the limit instead of HBM.  A lane
@@ -59,15 +60,14 @@ constexpr int kGroup = 8;      // tokens of a group
 constexpr int kMaxE = 512;     // LAROSA_MOE_MAX_E
 constexpr int kMaxK = 16;      // LAROSA_MOE_MAX_K
 constexpr int kMaxPairs = 16 * kMaxK;
-constexpr int kMaxParts = 16;  // CTAs a unit may span
+constexpr int kMinShare = 2;    // row steps of a share, at least
 constexpr int kCtasPerSm = 2;
 
 enum class Fmt { BF16, F32, MX4 };
 
-// Words of the workspace's zero-filled header: arrivals at the two barriers
-// and at the end, then the tickets of the two product phases.
-constexpr int kSyncA = 0, kSyncB = 1, kSyncEnd = 2;
-constexpr int kTickets1 = 16, kTickets2 = 1024;
+// Words of the workspace's zero-filled header: arrivals at the barriers and at
+// the end.
+constexpr int kBarriers = 4, kSyncEnd = kBarriers;
 
 struct MParams {
   const void* x;
@@ -102,10 +102,10 @@ struct Routing {
   short g_expert[kMaxPairs];
   short g_n[kMaxPairs];
   short g_pair[kMaxPairs][kGroup];
-  short parts[kMaxPairs];  // down: CTAs that a group's unit of the current tile spans
+  short group_of[kMaxPairs];
+  float join[kWarps][32];  // y: the experts' sums
   int groups;
   int ok;
-  unsigned order;
 };
 
 // ---------------------------------------------------------------- grid-wide barrier
@@ -339,6 +339,7 @@ __device__ void build_groups_warp(const MParams& p, Routing* r) {
   if (lane < pairs) {
     const int g = base + rank / kGroup;
     r->g_pair[g][rank % kGroup] = (short)lane;
+    r->group_of[lane] = (short)g;
     if (rank % kGroup == 0) {
       r->g_expert[g] = (short)e;
       r->g_n[g] = (short)min(kGroup, cnt - rank);
@@ -378,6 +379,7 @@ __device__ void build_groups(const MParams& p, Routing* r) {
     for (int o = 0; o < q; ++o) rank += r->expert[o] == e;
     const int g = r->base[e] + rank / kGroup;
     r->g_pair[g][rank % kGroup] = (short)q;
+    r->group_of[q] = (short)g;
     if (rank % kGroup == 0) {
       r->g_expert[g] = (short)e;
       r->g_n[g] = (short)min(kGroup, r->cnt[e] - rank);
@@ -388,8 +390,10 @@ __device__ void build_groups(const MParams& p, Routing* r) {
 
 // ---------------------------------------------------------------- products
 
-// One unit's operands: rows [k0, k1) of a matrix with `rows` rows and `ld`
-// columns, two column segments at cA and cB with `wA` and `wB` valid columns.
+// A warp's part of a unit: rows [k0, k1) of a matrix with `rows` rows and `ld`
+// columns.  bf16 and fp32: two segments of 64 columns at cA and cB, of which wA
+// and wB are valid; MX4: one of 128 at cA.  The sums of token i of the group,
+// column c of the unit go to out[i][c < 64 or MX4 ? cA + c : cB + c - 64].
 struct Unit {
   const uint8_t* W;       // the expert's matrix (MX4: codes)
   const uint8_t* scales;  // MX4
@@ -400,28 +404,13 @@ struct Unit {
 };
 
 template <Fmt F>
-struct Cfg;
-template <>
-struct Cfg<Fmt::BF16> {
-  static constexpr int kSeg = 64;    // columns of a segment
-  static constexpr int kStep = 16;   // rows a warp takes at a time
-  static constexpr size_t kSmem = (size_t)kWarps * kGroup * 2 * kSeg * 4;
-};
-template <>
-struct Cfg<Fmt::F32> {
-  static constexpr int kSeg = 64;
-  static constexpr int kStep = 32;
-  static constexpr size_t kCoef = (size_t)kWarps * 32 * kGroup * 4;  // a warp's 32 rows of coefficients
-  static constexpr size_t kSmem = (size_t)kWarps * kGroup * 2 * kSeg * 4 + kCoef;
-};
-template <>
-struct Cfg<Fmt::MX4> {
-  static constexpr int kSeg = 128;
-  static constexpr int kStep = 32;
-  static constexpr int kRing = 3;  // tiles of a warp's ring
-  static constexpr size_t kRingBytes = (size_t)kWarps * kRing * sizeof(mx4::Tile);
-  static constexpr size_t kPart = (size_t)kWarps * kGroup * kSeg * 4;  // a segment's sums of every warp
-  static constexpr size_t kSmem = kRingBytes + kPart + (size_t)kGroup * 2 * kSeg * 4;
+struct Cfg {
+  static constexpr int kStep = F == Fmt::BF16 ? 16 : 32;  // rows of a step
+  static constexpr int kRing = 4;                         // MX4: tiles of a warp's ring
+  static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
+                                      : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
+                                                      : kRing * sizeof(mx4::Tile);
+  static constexpr size_t kSmem = kWarps * kWarpSmem;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
@@ -431,34 +420,34 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
 
-// bf16 weights: sums of this warp's rows to part[warp][token][column].  The
-// operand of the token in column g of B is P rows of `stride` bf16 values at
-// `op` (null: no token).
+// bf16 weights.  The operand of the token in column g of B is P rows of
+// u.rows bf16 values at `op` (null: no token); o0, o1: where the sums of tokens
+// 2 t and 2 t + 1 go (null: nowhere).
 template <int P>
-__device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16* op, int stride, float* part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16* op, float* o0, float* o1) {
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const bool inA = 8 * g < u.wA, inB = 8 * g < u.wB;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const size_t row_bytes = (size_t)u.ld * 2;
+  const uint32_t row_bytes = (uint32_t)u.ld * 2;
   const uint8_t* base = u.W + (size_t)(4 * t) * row_bytes;
-  const size_t offA = (size_t)(u.cA + 8 * g) * 2, offB = (size_t)(u.cB + 8 * g) * 2;
+  const uint32_t offA = (uint32_t)(u.cA + 8 * g) * 2, offB = (uint32_t)(u.cB + 8 * g) * 2;
   float acc[2][4][4] = {};
   struct Rows {
     uint4 w[2][4];
     uint2 b[P];
   };
   auto load = [&](int r0, Rows& s) {
-    const bool in = r0 + 4 * t < u.k1;  // rows and splits are multiples of four
+    const bool in = r0 + 4 * t < u.k1;  // rows are multiples of four
     const uint8_t* at = base + (size_t)r0 * row_bytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s.w[0][i] = in && inA ? __ldcs(reinterpret_cast<const uint4*>(at + i * row_bytes + offA)) : zero;
-      s.w[1][i] = in && inB ? __ldcs(reinterpret_cast<const uint4*>(at + i * row_bytes + offB)) : zero;
+      s.w[0][i] = in && inA ? __ldcs(reinterpret_cast<const uint4*>(at + (size_t)i * row_bytes + offA)) : zero;
+      s.w[1][i] = in && inB ? __ldcs(reinterpret_cast<const uint4*>(at + (size_t)i * row_bytes + offB)) : zero;
     }
 #pragma unroll
     for (int q = 0; q < P; ++q)
-      s.b[q] = in && op != nullptr ? *reinterpret_cast<const uint2*>(op + (size_t)q * stride + r0 + 4 * t)
+      s.b[q] = in && op != nullptr ? *reinterpret_cast<const uint2*>(op + (size_t)q * u.rows + r0 + 4 * t)
                                    : make_uint2(0u, 0u);
   };
   auto multiply = [&](const Rows& s) {
@@ -476,58 +465,72 @@ __device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16*
         for (int c = 0; c < P; ++c) mma_bf16(acc[seg][q], a0, a1, a2, a3, s.b[c]);
       }
   };
-  constexpr int kStride = kWarps * 16;
+  // two steps in turn, each loaded while the other is multiplied
   Rows s0, s1;
-  int r = u.k0 + warp * 16;
-  if (r < u.k1) load(r, s0);
-  while (r < u.k1) {
-    if (r + kStride < u.k1) load(r + kStride, s1);
+  int r = u.k0;
+  load(r, s0);
+  while (true) {
+    if (r + 16 < u.k1) load(r + 16, s1);
     multiply(s0);
-    r += kStride;
+    r += 16;
     if (r >= u.k1) break;
-    if (r + kStride < u.k1) load(r + kStride, s0);
+    if (r + 16 < u.k1) load(r + 16, s0);
     multiply(s1);
-    r += kStride;
+    r += 16;
+    if (r >= u.k1) break;
   }
 #pragma unroll
-  for (int seg = 0; seg < 2; ++seg)
+  for (int seg = 0; seg < 2; ++seg) {
+    if (!(seg == 0 ? inA : inB)) continue;
+    const int c = (seg == 0 ? u.cA : u.cB) + 8 * g;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float* at = part + ((size_t)warp * kGroup + 2 * t) * 128 + 64 * seg + 8 * g + 2 * q;
-      *reinterpret_cast<float2*>(at) = make_float2(acc[seg][q][0], acc[seg][q][2]);
-      *reinterpret_cast<float2*>(at + 128) = make_float2(acc[seg][q][1], acc[seg][q][3]);
+    for (int q = 0; q < 4; q += 2) {
+      if (o0 != nullptr)
+        __stcg(reinterpret_cast<float4*>(o0 + c + 2 * q),
+               make_float4(acc[seg][q][0], acc[seg][q][2], acc[seg][q + 1][0], acc[seg][q + 1][2]));
+      if (o1 != nullptr)
+        __stcg(reinterpret_cast<float4*>(o1 + c + 2 * q),
+               make_float4(acc[seg][q][1], acc[seg][q][3], acc[seg][q + 1][1], acc[seg][q + 1][3]));
     }
+  }
 }
 
 // fp32 weights: lanes 0-15 hold four columns each of segment A, the others of
-// B; the rows' coefficients of every token lie in the warp's part of `coef`.
+// B; 32 rows' coefficients of every token lie in the warp's shared memory.
+// op[i], out[i]: coefficients and sums of token i.
 template <int N>
-__device__ __forceinline__ void product_f32(const Unit& u, const float* const (&op)[kGroup], float* coef, float* part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void product_f32(const Unit& u, const float* const (&op)[kGroup],
+                                            float* const (&out)[kGroup], float* coef) {
+  const int lane = threadIdx.x & 31;
   const int seg = lane >> 4, c = 4 * (lane & 15);
   const bool in = c < (seg == 0 ? u.wA : u.wB);
-  const float* base = reinterpret_cast<const float*>(u.W) + (seg == 0 ? u.cA : u.cB) + c;
-  float* mine = coef + warp * 32 * kGroup;  // [row][token]
+  const int col = (seg == 0 ? u.cA : u.cB) + c;
+  const float* base = reinterpret_cast<const float*>(u.W) + col;
   float acc[N][4] = {};
-  for (int r0 = u.k0 + warp * 32; r0 < u.k1; r0 += kWarps * 32) {
-    __syncwarp();
-#pragma unroll
-    for (int m = 0; m < N; ++m)
-      mine[lane * kGroup + m] = op[m] != nullptr && r0 + lane < u.k1 ? op[m][r0 + lane] : 0.f;
-    __syncwarp();
+  constexpr int kBatch = 8;  // rows in flight
+  for (int r0 = u.k0; r0 < u.k1; r0 += 32) {
     const int n = min(32, u.k1 - r0);
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 8) {
-      float4 w[8];
+    float4 w[kBatch];
+    auto load = [&](int i0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kBatch; ++i)
         w[i] = in && i0 + i < n ? __ldcs(reinterpret_cast<const float4*>(base + (size_t)(r0 + i0 + i) * u.ld))
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+    for (int m = 0; m < N; ++m)  // [row][token]
+      coef[lane * kGroup + m] = op[m] != nullptr && lane < n ? op[m][r0 + lane] : 0.f;
+    __syncwarp();
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      if (i0 > 0) load(i0);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
 #pragma unroll
         for (int m = 0; m < N; ++m) {
-          const float v = mine[(i0 + i) * kGroup + m];
+          const float v = coef[(i0 + i) * kGroup + m];
           acc[m][0] = fmaf(v, w[i].x, acc[m][0]);
           acc[m][1] = fmaf(v, w[i].y, acc[m][1]);
           acc[m][2] = fmaf(v, w[i].z, acc[m][2]);
@@ -537,172 +540,146 @@ __device__ __forceinline__ void product_f32(const Unit& u, const float* const (&
   }
 #pragma unroll
   for (int m = 0; m < N; ++m)
-    *reinterpret_cast<float4*>(part + ((size_t)warp * kGroup + m) * 128 + 64 * seg + c) =
-        make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+    if (in && out[m] != nullptr)
+      __stcg(reinterpret_cast<float4*>(out[m] + col), make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]));
 }
 
-// MX4 weights: blocks of 32 rows by 128 columns through the warp's ring of
-// tiles, segment A's, then B's, in one stream; after a segment the warps' sums
-// are added, in warp order, into sums[token][256].
+// MX4 weights: blocks of 32 rows through the warp's ring of tiles.
 //   kEight   op: pieces of the token in column g of B (token g), the second
-//            `rows` halves after the first; sx: block scales of the tokens 2 t
-//            and 2 t + 1
-//   else     up to four tokens; op: piece g % 2 of token g / 2; sx[0]: of token t
+//            u.rows halves after the first; sx: block scales of the tokens 2 t
+//            and 2 t + 1, o: where their sums go
+//   else     up to four tokens; op: piece g % 2 of token g / 2; sx[0], o[0]: of
+//            token t
 // Null: no token.
 template <bool kEight>
 __device__ __forceinline__ void product_mx4(const Unit& u, const __half* op, const float* const (&sx)[2],
-                                            unsigned char* smem) {
-  using C = Cfg<Fmt::MX4>;
-  constexpr int kRing = C::kRing;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+                                            float* const (&o)[2], mx4::Tile* ring) {
+  constexpr int kRing = Cfg<Fmt::MX4>::kRing;
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  mx4::Tile* ring = reinterpret_cast<mx4::Tile*>(smem) + warp * kRing;
-  float* part = reinterpret_cast<float*>(smem + C::kRingBytes);
-  float* sums = reinterpret_cast<float*>(smem + C::kRingBytes + C::kPart);
-  const int first = u.k0 / 32 + warp, last = u.k1 / 32;
-  const int mine = first < last ? (last - first + kWarps - 1) / kWarps : 0;  // this warp's blocks
-  const int segs = u.wB > 0 ? 2 : 1;
-
+  const int first = u.k0 / 32, blocks = (u.k1 - u.k0) / 32;
   mx4::BlockCopies copies;
-  copies.start(u.W, u.scales, u.ld, u.cA, u.wA, first, kWarps, lane);
-  int issued = 0, fill = 0;
-  auto issue = [&]() {
-    if (issued < mine * segs) {
-      if (issued == mine) copies.start(u.W, u.scales, u.ld, u.cB, u.wB, first, kWarps, lane);
-      copies.next(ring[fill], lane);
-    }
-    ++issued;
-    fill = fill + 1 == kRing ? 0 : fill + 1;
-    mx4::copies_commit();
-  };
+  copies.start(u.W, u.scales, u.ld, u.cA, u.wA, first, 1, lane);
   struct Ops {
     uint2 b[2][2];  // [step][piece]; up to four tokens: [step][0]
     float s[2];
   };
-  auto load_ops = [&](int i, Ops& o) {
-    const int b = first + i * kWarps;
+  const __half* op_at = op != nullptr ? op + first * 32 + 4 * t : nullptr;
+  auto load_ops = [&](int i, Ops& v) {
+    const bool in = i < blocks;
 #pragma unroll
     for (int step = 0; step < 2; ++step)
 #pragma unroll
       for (int piece = 0; piece < (kEight ? 2 : 1); ++piece)
-        o.b[step][piece] = op != nullptr && i < mine ? *reinterpret_cast<const uint2*>(
-                                                            op + (size_t)piece * u.rows + b * 32 + 16 * step + 4 * t)
-                                                     : make_uint2(0u, 0u);
+        v.b[step][piece] = in && op_at != nullptr ? *reinterpret_cast<const uint2*>(
+                                                        op_at + (size_t)piece * u.rows + i * 32 + 16 * step)
+                                                  : make_uint2(0u, 0u);
 #pragma unroll
-    for (int i2 = 0; i2 < (kEight ? 2 : 1); ++i2) o.s[i2] = sx[i2] != nullptr && i < mine ? sx[i2][b] : 0.f;
+    for (int j = 0; j < (kEight ? 2 : 1); ++j) v.s[j] = in && sx[j] != nullptr ? sx[j][first + i] : 0.f;
   };
+  __syncwarp();  // the part before has read its tiles
 #pragma unroll
-  for (int s = 0; s < kRing - 1; ++s) issue();
-  int now = 0;
-  for (int seg = 0; seg < segs; ++seg) {
-    unsigned long long acc8[1][16];
-    float acc4[1][8][2];
+  for (int s = 0; s < kRing - 1; ++s) {
+    if (s < blocks) copies.next(ring[s], lane);
+    mx4::copies_commit();
+  }
+  unsigned long long acc8[1][16];
+  float acc4[1][8][2];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      acc8[0][c] = 0ull;
-      acc4[0][c / 2][c % 2] = 0.f;
-    }
-    Ops cur;
-    load_ops(0, cur);
+  for (int c = 0; c < 16; ++c) {
+    acc8[0][c] = 0ull;
+    acc4[0][c / 2][c % 2] = 0.f;
+  }
+  Ops cur;
+  load_ops(0, cur);
+  int now = 0, fill = kRing - 1;
 #pragma unroll 1
-    for (int i = 0; i < mine; ++i) {
-      __syncwarp();  // every lane has read the tile that is filled next
-      issue();
-      Ops next;
-      load_ops(i + 1, next);
-      mx4::copies_wait<kRing - 1>();
-      __syncwarp();  // the other lanes' copies too
-      mx4::RowSet rs;
-      rs.read<4, 4>(ring[now], g, t);
-      now = now + 1 == kRing ? 0 : now + 1;
-      if constexpr (kEight) {
-        const uint2 b[2][1][2] = {{{cur.b[0][0], cur.b[0][1]}}, {{cur.b[1][0], cur.b[1][1]}}};
-        const unsigned long long s2[1] = {mx4::pack2(cur.s[0], cur.s[1])};
-        mx4::block_product8<1>(rs, b, s2, acc8);
-      } else {
-        const uint2 b[2][1] = {{cur.b[0][0]}, {cur.b[1][0]}};
-        const float s1[1] = {cur.s[0]};
-        mx4::block_product<1, 4, 4>(rs, b, s1, acc4);
-      }
-      cur = next;
-    }
-    // [warp][token][column]
+  for (int i = 0; i < blocks; ++i) {
+    __syncwarp();  // every lane has read the tile that is filled next
+    if (i + kRing - 1 < blocks) copies.next(ring[fill], lane);
+    mx4::copies_commit();
+    Ops next;
+    load_ops(i + 1, next);
+    mx4::copies_wait<kRing - 1>();
+    __syncwarp();  // the other lanes' copies too
+    mx4::RowSet rs;
+    rs.read<4, 4>(ring[now], g, t);
+    now = now + 1 == kRing ? 0 : now + 1;
+    fill = fill + 1 == kRing ? 0 : fill + 1;
     if constexpr (kEight) {
-      float* at = part + ((size_t)warp * kGroup + 2 * t) * C::kSeg + 16 * g;
-#pragma unroll
-      for (int c = 0; c < 16; c += 4) {
-        const float2 v[4] = {mx4::unpack2(acc8[0][c]), mx4::unpack2(acc8[0][c + 1]), mx4::unpack2(acc8[0][c + 2]),
-                             mx4::unpack2(acc8[0][c + 3])};
-        *reinterpret_cast<float4*>(at + c) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
-        *reinterpret_cast<float4*>(at + C::kSeg + c) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
-      }
+      const uint2 b[2][1][2] = {{{cur.b[0][0], cur.b[0][1]}}, {{cur.b[1][0], cur.b[1][1]}}};
+      const unsigned long long s2[1] = {mx4::pack2(cur.s[0], cur.s[1])};
+      mx4::block_product8<1>(rs, b, s2, acc8);
     } else {
-      float* at = part + ((size_t)warp * kGroup + t) * C::kSeg + 16 * g;
-#pragma unroll
-      for (int q = 0; q < 8; q += 2)
-        *reinterpret_cast<float4*>(at + 2 * q) =
-            make_float4(acc4[0][q][0], acc4[0][q][1], acc4[0][q + 1][0], acc4[0][q + 1][1]);
+      const uint2 b[2][1] = {{cur.b[0][0]}, {cur.b[1][0]}};
+      const float s1[1] = {cur.s[0]};
+      mx4::block_product<1, 4, 4>(rs, b, s1, acc4);
     }
-    __syncthreads();
-    for (int e = tid; e < u.n * C::kSeg; e += kT) {
-      float s = part[e];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) s += part[(size_t)w * kGroup * C::kSeg + e];
-      sums[(e / C::kSeg) * 2 * C::kSeg + seg * C::kSeg + e % C::kSeg] = s;
-    }
-    __syncthreads();
+    cur = next;
   }
   mx4::copies_wait<0>();
+  if (16 * g >= u.wA) return;
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    const int col = u.cA + 16 * g + c;
+    if constexpr (kEight) {
+      const float2 v[4] = {mx4::unpack2(acc8[0][c]), mx4::unpack2(acc8[0][c + 1]), mx4::unpack2(acc8[0][c + 2]),
+                           mx4::unpack2(acc8[0][c + 3])};
+      if (o[0] != nullptr) __stcg(reinterpret_cast<float4*>(o[0] + col), make_float4(v[0].x, v[1].x, v[2].x, v[3].x));
+      if (o[1] != nullptr) __stcg(reinterpret_cast<float4*>(o[1] + col), make_float4(v[0].y, v[1].y, v[2].y, v[3].y));
+    } else if (o[0] != nullptr) {
+      const int q = c / 2;
+      __stcg(reinterpret_cast<float4*>(o[0] + col),
+             make_float4(acc4[0][q][0], acc4[0][q][1], acc4[0][q + 1][0], acc4[0][q + 1][1]));
+    }
+  }
 }
 
-// Where the unit's sums over the CTA's warps lie: [token][2 kSeg].
-template <Fmt F>
-__device__ __forceinline__ float* unit_sums(unsigned char* smem) {
-  if constexpr (F == Fmt::MX4)
-    return reinterpret_cast<float*>(smem + Cfg<F>::kRingBytes + Cfg<F>::kPart);
-  else
-    return reinterpret_cast<float*>(smem);
-}
-
-// The unit's sums.  Operand of a pair: x's (gate | up: token q / k) or h's
-// (down: pair q).
+// A warp's part of a unit of `group`; the pairs' sums go to rows of `ld_out`
+// floats at out.  Operand of a pair: x's (gate | up: token q / k) or h's (down:
+// pair q).
 template <Fmt F, bool kDown>
-__device__ void unit_product(const MParams& p, const Routing* r, int group, const Unit& u, unsigned char* smem) {
-  constexpr int kCols = 2 * Cfg<F>::kSeg;
-  const int tid = threadIdx.x, lane = tid & 31;
+__device__ __forceinline__ void part_product(const MParams& p, const Routing* r, int group, const Unit& u, float* out,
+                                             int ld_out, unsigned char* smem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rows = u.rows;
-  float* part = reinterpret_cast<float*>(smem);
+  auto pair_of = [&](int pos) -> int { return pos < u.n ? r->g_pair[group][pos] : -1; };
   auto operand = [&](int pos) -> int {  // row of the operand of the group's pos-th pair, -1: none
-    if (pos >= u.n) return -1;
-    const int q = r->g_pair[group][pos];
-    return kDown ? q : q / p.k;
+    const int q = pair_of(pos);
+    return q < 0 || kDown ? q : q / p.k;
   };
-  __syncthreads();  // the sums of the unit before are used up
+  auto sums_of = [&](int pos) -> float* {
+    const int q = pair_of(pos);
+    return q < 0 ? nullptr : out + (size_t)q * ld_out;
+  };
   if constexpr (F == Fmt::BF16) {
     const int o = operand(g);
+    float* o0 = sums_of(2 * t);
+    float* o1 = sums_of(2 * t + 1);
     if constexpr (kDown)
-      product_bf16<3>(u, o < 0 ? nullptr : reinterpret_cast<const __nv_bfloat16*>(p.hop) + (size_t)o * 3 * rows, rows,
-                      part);
+      product_bf16<3>(u, o < 0 ? nullptr : reinterpret_cast<const __nv_bfloat16*>(p.hop) + (size_t)o * 3 * rows, o0, o1);
     else
-      product_bf16<1>(u, o < 0 ? nullptr : static_cast<const __nv_bfloat16*>(p.x) + (size_t)o * rows, rows, part);
+      product_bf16<1>(u, o < 0 ? nullptr : static_cast<const __nv_bfloat16*>(p.x) + (size_t)o * rows, o0, o1);
   } else if constexpr (F == Fmt::F32) {
     const float* src = kDown ? reinterpret_cast<const float*>(p.hop) : static_cast<const float*>(p.x);
     const float* op[kGroup];
+    float* to[kGroup];
 #pragma unroll
     for (int m = 0; m < kGroup; ++m) {
       const int o = operand(m);
       op[m] = o < 0 ? nullptr : src + (size_t)o * rows;
+      to[m] = sums_of(m);
     }
-    float* coef = part + (size_t)kWarps * kGroup * kCols;
+    float* coef = reinterpret_cast<float*>(smem + warp * Cfg<F>::kWarpSmem);
     if (u.n <= 1)
-      product_f32<1>(u, op, coef, part);
+      product_f32<1>(u, op, to, coef);
     else if (u.n <= 2)
-      product_f32<2>(u, op, coef, part);
+      product_f32<2>(u, op, to, coef);
     else if (u.n <= 4)
-      product_f32<4>(u, op, coef, part);
+      product_f32<4>(u, op, to, coef);
     else
-      product_f32<8>(u, op, coef, part);
+      product_f32<8>(u, op, to, coef);
   } else {
     const unsigned char* src = kDown ? p.hop : p.xop;
     const __half* pieces = reinterpret_cast<const __half*>(src);
@@ -711,25 +688,19 @@ __device__ void unit_product(const MParams& p, const Routing* r, int group, cons
       const int o = operand(pos);
       return o < 0 ? nullptr : scales + (size_t)o * (rows / 32);
     };
+    mx4::Tile* ring = reinterpret_cast<mx4::Tile*>(smem + warp * Cfg<F>::kWarpSmem);
     if (u.n <= 4) {
       const int o = operand(g >> 1);
       const float* const sx[2] = {scales_of(t), nullptr};
-      product_mx4<false>(u, o < 0 ? nullptr : pieces + ((size_t)o * 2 + (g & 1)) * rows, sx, smem);
+      float* const to[2] = {sums_of(t), nullptr};
+      product_mx4<false>(u, o < 0 ? nullptr : pieces + ((size_t)o * 2 + (g & 1)) * rows, sx, to, ring);
     } else {
       const int o = operand(g);
       const float* const sx[2] = {scales_of(2 * t), scales_of(2 * t + 1)};
-      product_mx4<true>(u, o < 0 ? nullptr : pieces + (size_t)o * 2 * rows, sx, smem);
+      float* const to[2] = {sums_of(2 * t), sums_of(2 * t + 1)};
+      product_mx4<true>(u, o < 0 ? nullptr : pieces + (size_t)o * 2 * rows, sx, to, ring);
     }
-    return;  // added up already
   }
-  __syncthreads();
-  for (int e = tid; e < u.n * kCols; e += kT) {
-    float s = part[e];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += part[(size_t)w * kGroup * kCols + e];
-    part[e] = s;  // this thread's own element
-  }
-  __syncthreads();
 }
 
 // h of pair q, column j: stored as the operand of the down product.  Lanes of
@@ -752,67 +723,77 @@ __device__ __forceinline__ void put_h(const MParams& p, int q, int j, float g, f
   }
 }
 
-// True in every thread of the CTA that arrives last of `count` at a ticket,
-// which is zero again then.
-__device__ __forceinline__ bool last_to_arrive(unsigned* ticket, unsigned count, Routing* r) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned order = atomic_add_acq_rel_gpu(ticket, 1u);
-    r->order = order;
-    if (order == count - 1u) *ticket = 0u;
-  }
-  __syncthreads();
-  return r->order == count - 1u;
-}
-
-// The line of warp steps of a phase: `units` units of `steps` each, cut into
-// `ctas` shares.
+// The line of row steps of a phase: `units` units of `steps` each, cut into
+// `shares`.
 struct Line {
   int steps;
   long long total;
-  int ctas;
+  int shares;
 
-  // A share is at least two steps per warp (a unit that one CTA can finish in
-  // that time is not worth a sum through the workspace), and a unit spans at
-  // most kMaxParts CTAs (a share is at least steps / (kMaxParts - 2)).
-  __host__ __device__ Line(int units, int steps_, int grid) : steps(steps_), total((long long)units * steps_) {
-    const long long by_share = total / (2 * kWarps), most = (long long)units * (kMaxParts - 2);
-    long long n = by_share < grid ? by_share : grid;
-    if (n > most) n = most;
-    ctas = n < 1 ? 1 : (int)n;
+  __host__ __device__ Line(int units, int steps_, int workers) : steps(steps_), total((long long)units * steps_) {
+    const long long n = total / kMinShare;
+    shares = n < 1 ? 1 : n < workers ? (int)n : workers;
   }
-  // a b / c; 32-bit division where the product allows it (a 64-bit one takes
-  // some hundred instructions)
-  static __device__ __forceinline__ long long mul_div(long long a, long long b, long long c) {
-    const long long n = a * b;
-    return n >> 32 == 0 ? (long long)((unsigned)n / (unsigned)c) : n / c;
+  // First step of a share; 32-bit division where the numbers allow it (a
+  // 64-bit one takes some hundred instructions).
+  __device__ __forceinline__ long long begin(int share) const {
+    const long long n = total * share;
+    return n >> 32 == 0 ? (long long)((unsigned)n / (unsigned)shares) : n / shares;
   }
-  __device__ __forceinline__ long long begin(int cta) const { return mul_div(total, cta, ctas); }
-  // The CTA whose share holds step `at`.
+  // The share that holds step `at`.
   __device__ __forceinline__ int owner(long long at) const {
-    const long long n = (at + 1) * ctas - 1;
+    const long long n = (at + 1) * shares - 1;
     return n >> 32 == 0 ? (int)((unsigned)n / (unsigned)total) : (int)(n / total);
   }
-  // Unit of step `at`.
   __device__ __forceinline__ int unit(long long at) const {
     return at >> 32 == 0 ? (int)((unsigned)at / (unsigned)steps) : (int)(at / steps);
   }
-  // Most CTAs a unit can span.
-  int parts() const { return (int)((steps + total / ctas - 1) / (total / ctas)) + 1; }
+  // Shares that unit u's steps lie in: first, and how many.
+  __device__ __forceinline__ int first(int u) const { return owner((long long)u * steps); }
+  __device__ __forceinline__ int parts(int u) const { return owner((long long)(u + 1) * steps - 1) - first(u) + 1; }
+  // The most parts a unit can have.
+  int most_parts() const { return (int)((steps + total / shares - 1) / (total / shares)) + 1; }
 };
+
+// Sum of `n` parts, `step` floats apart, in order.
+__device__ __forceinline__ float add_parts(const float* from, size_t step, int n) {
+  float s = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 16) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i0 + i < n ? __ldcg(from + (size_t)(i0 + i) * step) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += v[i];
+  }
+  return s;
+}
 
 template <Fmt F>
 __device__ __forceinline__ size_t row_bytes_of(int cols) {
   return F == Fmt::BF16 ? (size_t)cols * 2 : F == Fmt::F32 ? (size_t)cols * 4 : (size_t)cols / 2;
 }
 
+// The down rows that a share starts with, on their way to L2.
+template <Fmt F>
+__device__ __forceinline__ void prefetch_rows(const Unit& u, int lane) {
+  const size_t row = row_bytes_of<F>(u.ld), c0 = row_bytes_of<F>(u.cA);
+  const size_t width = row_bytes_of<F>(u.wA + u.wB);
+  const int lines = (int)((width + 127) / 128);
+  for (int i = lane; i < (u.k1 - u.k0) * lines; i += 32) {
+    const uint8_t* from = u.W + (size_t)(u.k0 + i / lines) * row + c0 + min((size_t)(i % lines) * 128, width - 1);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
+  }
+}
+
 template <Fmt F>
 __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Routing r;
-  constexpr int kSeg = Cfg<F>::kSeg, kCols = 2 * kSeg, kStep = Cfg<F>::kStep;
+  constexpr int kStep = Cfg<F>::kStep;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = p.M * p.k;
+  // shares are dealt over the CTAs first, so that few of them land on many SMs
+  const int me = warp * gridDim.x + blockIdx.x, workers = kWarps * gridDim.x;
 
   pdl_wait();
   pdl_launch_dependents();
@@ -825,7 +806,7 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
     scores<__nv_bfloat16>(p, &r);
   if constexpr (F == Fmt::MX4) {
     const int blocks = p.d / 32;
-    for (int i = warp * gridDim.x + blockIdx.x; i < p.M * blocks; i += kWarps * gridDim.x) {
+    for (int i = me; i < p.M * blocks; i += workers) {
       const int m = i / blocks, b = i % blocks;
       const size_t at = (size_t)m * p.d + b * 32 + lane;
       const float v = x_f32 ? static_cast<const float*>(p.x)[at]
@@ -833,7 +814,7 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
       put_pieces(p.xop, p.M, p.d, m, b, v, lane);
     }
   }
-  if (!grid_barrier(p.sync + kSyncA, &r, p)) return;
+  if (!grid_barrier(p.sync, &r, p)) return;
 
   // ------------------------------------------------------------------ routing
   for (int m = warp; m < p.M; m += kWarps) {
@@ -854,177 +835,124 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   const int G = r.groups;
 
   // ------------------------------------------------------------------ gate | up
-  const float* part = unit_sums<F>(smem);
-  {
-    const int tiles = (p.f + kSeg - 1) / kSeg;
-    const Line line(G * tiles, (p.d + kStep - 1) / kStep, gridDim.x);
+  // units: tile, group and, MX4, half (gate, up), the last fastest
+  constexpr int kTile1 = F == Fmt::MX4 ? 128 : 64, kHalves = F == Fmt::MX4 ? 2 : 1;
+  const Line up(G * kHalves * ((p.f + kTile1 - 1) / kTile1), (p.d + kStep - 1) / kStep, workers);
+  const size_t up_slab = (size_t)pairs * 2 * p.f;
+  if (me < up.shares) {
     const size_t expert_bytes = row_bytes_of<F>(2 * p.f) * p.d;
-    const int me = blockIdx.x;
-    long long at = me < line.ctas ? line.begin(me) : 0;
-    const long long stop = me < line.ctas ? line.begin(me + 1) : 0;
-    while (at < stop) {
-      const int w = line.unit(at), s0 = (int)(at - (long long)w * line.steps);
-      const int s1 = (int)min((long long)line.steps, s0 + (stop - at));
-      const int group = w % G, tile = w / G;
+    const long long stop = up.begin(me + 1);
+    for (long long at = up.begin(me); at < stop;) {
+      const int w = up.unit(at), s0 = (int)(at - (long long)w * up.steps);
+      const int s1 = (int)min((long long)up.steps, s0 + (stop - at));
+      const int group = w / kHalves % G, tile = w / kHalves / G, half = w % kHalves;
       const int e = r.g_expert[group];
       Unit u;
       u.W = p.gu + (size_t)e * expert_bytes;
       u.scales = F == Fmt::MX4 ? p.gus + (size_t)e * (p.d / 32) * (2 * p.f) : nullptr;
       u.rows = p.d;
       u.ld = 2 * p.f;
-      u.cA = tile * kSeg;
-      u.cB = p.f + tile * kSeg;
-      u.wA = u.wB = min(kSeg, p.f - tile * kSeg);
+      u.cA = tile * kTile1 + half * p.f;
+      u.cB = p.f + tile * kTile1;
+      u.wA = min(kTile1, p.f - tile * kTile1);
+      u.wB = F == Fmt::MX4 ? 0 : u.wA;
       u.n = r.g_n[group];
       u.k0 = s0 * kStep;
       u.k1 = min(p.d, s1 * kStep);
-      unit_product<F, false>(p, &r, group, u, smem);
+      part_product<F, false>(p, &r, group, u, p.part1 + (size_t)(me - up.first(w)) * up_slab, 2 * p.f, smem);
       at += s1 - s0;
-      if (s0 == 0 && s1 == line.steps) {
-        for (int i = tid; i < u.n * kSeg; i += kT) {
-          const int pos = i / kSeg, j = i % kSeg;
-          if (j < u.wA)
-            put_h<F>(p, r.g_pair[group][pos], u.cA + j, part[pos * kCols + j], part[pos * kCols + kSeg + j], lane);
-        }
-        continue;
-      }
-      // the unit spans CTAs first ... first + parts - 1
-      const int first = line.owner((long long)w * line.steps);
-      const int parts = line.owner((long long)(w + 1) * line.steps - 1) - first + 1;
-      for (int i = tid; i < u.n * kCols; i += kT) {
-        const int pos = i / kCols, c = i % kCols, j = c % kSeg;
-        if (j < u.wA)
-          __stcg(p.part1 + ((size_t)(me - first) * pairs + r.g_pair[group][pos]) * (2 * p.f) +
-                     (c < kSeg ? u.cA : u.cB) + j,
-                 part[i]);
-      }
-      if (!last_to_arrive(p.sync + kTickets1 + first, parts, &r)) continue;
-      for (int i = tid; i < u.n * kSeg; i += kT) {
-        const int pos = i / kSeg, j = i % kSeg;
-        if (j >= u.wA) continue;
-        const int q = r.g_pair[group][pos];
-        const float* from = p.part1 + (size_t)q * (2 * p.f) + u.cA + j;
-        const size_t step = (size_t)pairs * (2 * p.f);
-        float ga = 0.f, up = 0.f;
-        for (int part0 = 0; part0 < parts; part0 += 4) {
-          float a[4], b[4];
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            a[s] = part0 + s < parts ? __ldcg(from + (part0 + s) * step) : 0.f;
-            b[s] = part0 + s < parts ? __ldcg(from + (part0 + s) * step + p.f) : 0.f;
-          }
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            ga += a[s];
-            up += b[s];
-          }
-        }
-        put_h<F>(p, q, u.cA + j, ga, up, lane);
-      }
     }
   }
 
   // ------------------------------------------------------------------ down
-  const int tiles = (p.d + kCols - 1) / kCols;
-  const Line line(G * tiles, (p.f + kStep - 1) / kStep, gridDim.x);
-  const int me = blockIdx.x;
-  long long at = me < line.ctas ? line.begin(me) : 0;
-  const long long stop = me < line.ctas ? line.begin(me + 1) : 0;
+  const Line down(G * ((p.d + 127) / 128), (p.f + kStep - 1) / kStep, workers);
+  const size_t down_slab = (size_t)pairs * p.d;
+  long long at = me < down.shares ? down.begin(me) : 0;
+  const long long stop = me < down.shares ? down.begin(me + 1) : 0;
   const size_t expert_bytes = row_bytes_of<F>(p.d) * p.f;
-  // this CTA's part of the unit at step `at`
-  auto make_unit = [&](int* group, int* tile, int* s0, int* s1) {
-    const int w = line.unit(at);
-    *group = w % G;
-    *tile = w / G;
-    *s0 = (int)(at - (long long)w * line.steps);
-    *s1 = (int)min((long long)line.steps, *s0 + (stop - at));
-    const int e = r.g_expert[*group];
+  // this share's part of the unit at step `at`
+  auto make_unit = [&](int* w, int* s1) {
+    *w = down.unit(at);
+    const int s0 = (int)(at - (long long)*w * down.steps);
+    *s1 = (int)min((long long)down.steps, s0 + (stop - at));
+    const int group = *w % G, tile = *w / G;
+    const int e = r.g_expert[group];
     Unit u;
     u.W = p.dn + (size_t)e * expert_bytes;
     u.scales = F == Fmt::MX4 ? p.dns + (size_t)e * (p.f / 32) * p.d : nullptr;
     u.rows = p.f;
     u.ld = p.d;
-    u.cA = *tile * kCols;
-    u.cB = u.cA + kSeg;
-    u.wA = min(kSeg, p.d - u.cA);
-    u.wB = max(0, min(kSeg, p.d - u.cB));
-    u.n = r.g_n[*group];
-    u.k0 = *s0 * kStep;
+    u.cA = tile * 128;
+    u.cB = u.cA + 64;
+    u.wA = F == Fmt::MX4 ? min(128, p.d - u.cA) : min(64, p.d - u.cA);
+    u.wB = F == Fmt::MX4 ? 0 : max(0, min(64, p.d - u.cB));
+    u.n = r.g_n[group];
+    u.k0 = s0 * kStep;
     u.k1 = min(p.f, *s1 * kStep);
     return u;
   };
-  int group, tile, s0, s1;
-  if (at < stop) {
-    // the first rows on their way to L2 while the grid assembles
-    const Unit u = make_unit(&group, &tile, &s0, &s1);
-    const size_t row = row_bytes_of<F>(p.d);
-    const size_t c0 = row_bytes_of<F>(u.cA), width = row_bytes_of<F>(u.wA + u.wB);
-    const int lines = (int)((width + 127) / 128);
-    for (int i = tid; i < (u.k1 - u.k0) * lines; i += kT) {
-      const uint8_t* from = u.W + (size_t)(u.k0 + i / lines) * row + c0 + min((size_t)(i % lines) * 128, width - 1);
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
+  int w, s1;
+  if (at < stop) prefetch_rows<F>(make_unit(&w, &s1), lane);
+  if (!grid_barrier(p.sync + 1, &r, p)) return;
+  // h, 32 columns of a pair per warp: the parts of gate and of up joined
+  {
+    const int chunks = (p.f + 31) / 32;
+    for (int i = me; i < pairs * chunks; i += workers) {
+      const int q = i / chunks, j = i % chunks * 32 + lane;
+      const int unit = (j / kTile1 * G + r.group_of[q]) * kHalves;
+      const float* from = p.part1 + (size_t)q * 2 * p.f + j;
+      // MX4: f is a multiple of 32, every lane has a column
+      if (j < p.f) {
+        const int n = up.parts(unit);
+        const float g = add_parts(from, up_slab, n);
+        const float v = add_parts(from + p.f, up_slab, kHalves == 2 ? up.parts(unit + 1) : n);
+        put_h<F>(p, q, j, g, v, lane);
+      }
     }
   }
-  if (!grid_barrier(p.sync + kSyncB, &r, p)) return;
+  if (!grid_barrier(p.sync + 2, &r, p)) return;
   while (at < stop) {
-    const Unit u = make_unit(&group, &tile, &s0, &s1);
-    unit_product<F, true>(p, &r, group, u, smem);
-    const long long unit_at = at - s0;
-    at += s1 - s0;
-    const int first = line.owner(unit_at);
-    for (int i = tid; i < u.n * kCols; i += kT) {
-      const int pos = i / kCols, c = i % kCols;
-      if (u.cA + c < p.d)
-        __stcg(p.part2 + ((size_t)(me - first) * pairs + r.g_pair[group][pos]) * p.d + u.cA + c, part[i]);
-    }
-    // once per tile: after this CTA's last unit of it
-    const long long tile_at = (long long)tile * G * line.steps, tile_end = tile_at + (long long)G * line.steps;
-    if (at < stop && at < tile_end) continue;
-    const unsigned arrivals = (unsigned)(line.owner(tile_end - 1) - line.owner(tile_at) + 1);
-    if (!last_to_arrive(p.sync + kTickets2 + tile, arrivals, &r)) continue;
-    for (int g = tid; g < G; g += kT) {
-      const long long from = tile_at + (long long)g * line.steps;
-      const short parts = (short)(line.owner(from + line.steps - 1) - line.owner(from) + 1);
-      for (int i = 0; i < r.g_n[g]; ++i) r.parts[r.g_pair[g][i]] = parts;
-    }
-    __syncthreads();
-    const int width = min(kCols, p.d - u.cA);
-    for (int i = tid; i < p.M * width; i += kT) {
-      const int m = i / width, c = u.cA + i % width;
+    const Unit u = make_unit(&w, &s1);
+    part_product<F, true>(p, &r, w % G, u, p.part2 + (size_t)(me - down.first(w)) * down_slab, p.d, smem);
+    at = (long long)w * down.steps + s1;
+  }
+  if (!grid_barrier(p.sync + 3, &r, p)) return;
+
+  // ------------------------------------------------------------------ y
+  // 32 columns of a token by `team` warps: warp i of the team joins the parts
+  // of the experts i, i + team, ...; their sums are added in the experts' order
+  {
+    const int team = p.k >= 8 ? 8 : p.k >= 4 ? 4 : p.k >= 2 ? 2 : 1;
+    const int chunks = (p.d + 31) / 32, tasks = p.M * chunks;
+    const int i_team = warp % team, per_cta = kWarps / team;
+    for (int base = blockIdx.x * per_cta; base < tasks; base += gridDim.x * per_cta) {
+      const int task = base + warp / team;
+      const int m = task / chunks, c = task % chunks * 32 + lane;
+      const bool in = task < tasks && c < p.d;
       float y = 0.f;
-      // eight experts' first two parts in flight; further parts are rare
-      for (int q0 = m * p.k; q0 < (m + 1) * p.k; q0 += 8) {
-        const int n = min(8, (m + 1) * p.k - q0);
-        float v[8][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            v[i][s] = i < n && s < r.parts[q0 + i]
-                          ? __ldcg(p.part2 + ((size_t)s * pairs + q0 + i) * p.d + c) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= n) break;
-          float sum = v[i][0] + v[i][1];
-          for (int s = 2; s < r.parts[q0 + i]; ++s) sum += __ldcg(p.part2 + ((size_t)s * pairs + q0 + i) * p.d + c);
-          y = fmaf(r.gate[q0 + i], sum, y);
+      for (int s0 = 0; s0 < p.k; s0 += team) {
+        const int s = s0 + i_team;
+        float v = 0.f;
+        if (in && s < p.k) {
+          const int q = m * p.k + s;
+          v = add_parts(p.part2 + (size_t)q * p.d + c, down_slab, down.parts(c / 128 * G + r.group_of[q]));
         }
+        r.join[warp][lane] = v;
+        __syncthreads();
+        if (i_team == 0 && in)
+          for (int i = 0; i < team && s0 + i < p.k; ++i) y = fmaf(r.gate[m * p.k + s0 + i], r.join[warp + i][lane], y);
+        __syncthreads();
       }
-      p.y[(size_t)m * p.d + c] = y;
+      if (i_team == 0 && in) p.y[(size_t)m * p.d + c] = y;
     }
-    __syncthreads();  // r.parts is read
   }
 
-  // the barriers' words are zero again once every CTA has passed both
-  __syncthreads();
+  // the barriers' words are zero again once every CTA has passed the last one
   if (tid == 0 && atomic_add_acq_rel_gpu(p.sync + kSyncEnd, 1u) == gridDim.x - 1u) {
-    p.sync[kSyncA] = 0u;
-    p.sync[kSyncB] = 0u;
-    p.sync[kSyncEnd] = 0u;
+#pragma unroll
+    for (int i = 0; i <= kBarriers; ++i) p.sync[i] = 0u;
   }
 }
-
-int seg_of(MoeFormat f) { return f == MoeFormat::MX4 ? 128 : 64; }
 
 struct MoePlan {
   size_t logits, xop, hop, part1, part2, total;
@@ -1032,13 +960,15 @@ struct MoePlan {
 
 MoePlan make_plan(int M, int d, int f, int E, int k, MoeFormat fmt) {
   MoePlan pl;
-  const int seg = seg_of(fmt), step = fmt == MoeFormat::BF16 ? 16 : 32;
-  const int grid = 148 * kCtasPerSm;
-  // A unit spans the most CTAs where there are the fewest units: there are at
+  const bool mx4 = fmt == MoeFormat::MX4;
+  const int step = fmt == MoeFormat::BF16 ? 16 : 32;
+  const int workers = 148 * kCtasPerSm * kWarps;
+  // A unit has the most parts where there are the fewest units: there are at
   // least k groups (a token's experts differ) and one for every eight pairs.
   const int groups = std::max(k, (M * k + kGroup - 1) / kGroup);
-  const int parts1 = Line(groups * ((f + seg - 1) / seg), (d + step - 1) / step, grid).parts();
-  const int parts2 = Line(groups * ((d + 2 * seg - 1) / (2 * seg)), (f + step - 1) / step, grid).parts();
+  const int units1 = groups * (mx4 ? 2 * ((f + 127) / 128) : (f + 63) / 64);
+  const int parts1 = Line(units1, (d + step - 1) / step, workers).most_parts();
+  const int parts2 = Line(groups * ((d + 127) / 128), (f + step - 1) / step, workers).most_parts();
   const size_t pairs = (size_t)M * k;
   size_t off = 0;
   auto take = [&](size_t bytes) {
