@@ -24,10 +24,9 @@
 //            two fp32 values are exact in fp64.)
 //   routing  every CTA makes the same selection and the same work list from
 //            the scores.  A group is an expert and up to eight of its tokens;
-//            a unit is a group and 128 columns (gate|up of bf16 and fp32: 64
-//            gate columns and the 64 up columns beside them).
+//            a unit is a group and 128 columns.
 //   products the row steps of all units, in order, are one line that is cut
-//            into equal shares, one per warp of the grid: how many units there
+//            into equal shares for the warps of the grid: how many units there
 //            are is known only after the routing (5 tokens of 60 experts made
 //            396 units for 296 CTAs), and a share is one long stream of rows
 //            with no barrier in it.  A warp writes the sums of its part of a
@@ -66,8 +65,9 @@ constexpr int kCtasPerSm = 2;
 enum class Fmt { BF16, F32, MX4 };
 
 // Words of the workspace's zero-filled header: arrivals at the barriers and at
-// the end.
-constexpr int kBarriers = 4, kSyncEnd = kBarriers;
+// the end, and shares taken beyond the first of every warp in the two product
+// phases.
+constexpr int kBarriers = 4, kSyncEnd = kBarriers, kTaken1 = 5, kTaken2 = 6, kSyncWords = 7;
 
 struct MParams {
   const void* x;
@@ -391,21 +391,20 @@ __device__ void build_groups(const MParams& p, Routing* r) {
 // ---------------------------------------------------------------- products
 
 // A warp's part of a unit: rows [k0, k1) of a matrix with `rows` rows and `ld`
-// columns.  bf16 and fp32: two segments of 64 columns at cA and cB, of which wA
-// and wB are valid; MX4: one of 128 at cA.  The sums of token i of the group,
-// column c of the unit go to out[i][c < 64 or MX4 ? cA + c : cB + c - 64].
+// columns, `width` columns (at most 128) from `col` on.
 struct Unit {
   const uint8_t* W;       // the expert's matrix (MX4: codes)
   const uint8_t* scales;  // MX4
   int rows, ld;
-  int cA, cB, wA, wB;
+  int col, width;
   int k0, k1;
   int n;  // tokens
 };
 
 template <Fmt F>
 struct Cfg {
-  static constexpr int kStep = F == Fmt::BF16 ? 16 : 32;  // rows of a step
+  static constexpr int kStep = F == Fmt::BF16 ? 16 : F == Fmt::F32 ? 8 : 32;  // rows of a step
+  static constexpr int kRounds = F == Fmt::MX4 ? 6 : 1;   // shares per warp
   static constexpr int kRing = 4;                         // MX4: tiles of a warp's ring
   static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
                                       : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
@@ -427,11 +426,12 @@ template <int P>
 __device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16* op, float* o0, float* o1) {
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const bool inA = 8 * g < u.wA, inB = 8 * g < u.wB;
+  // columns 8 g and 64 + 8 g of the unit
+  const bool inA = 8 * g < u.width, inB = 64 + 8 * g < u.width;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   const uint32_t row_bytes = (uint32_t)u.ld * 2;
   const uint8_t* base = u.W + (size_t)(4 * t) * row_bytes;
-  const uint32_t offA = (uint32_t)(u.cA + 8 * g) * 2, offB = (uint32_t)(u.cB + 8 * g) * 2;
+  const uint32_t offA = (uint32_t)(u.col + 8 * g) * 2, offB = offA + 128;
   float acc[2][4][4] = {};
   struct Rows {
     uint4 w[2][4];
@@ -482,7 +482,7 @@ __device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16*
 #pragma unroll
   for (int seg = 0; seg < 2; ++seg) {
     if (!(seg == 0 ? inA : inB)) continue;
-    const int c = (seg == 0 ? u.cA : u.cB) + 8 * g;
+    const int c = u.col + 64 * seg + 8 * g;
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
       if (o0 != nullptr)
@@ -495,47 +495,58 @@ __device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16*
   }
 }
 
-// fp32 weights: lanes 0-15 hold four columns each of segment A, the others of
-// B; 32 rows' coefficients of every token lie in the warp's shared memory.
+// fp32 weights: a lane holds four columns; 32 rows' coefficients of every token
+// lie in the warp's shared memory.
 // op[i], out[i]: coefficients and sums of token i.
 template <int N>
 __device__ __forceinline__ void product_f32(const Unit& u, const float* const (&op)[kGroup],
                                             float* const (&out)[kGroup], float* coef) {
   const int lane = threadIdx.x & 31;
-  const int seg = lane >> 4, c = 4 * (lane & 15);
-  const bool in = c < (seg == 0 ? u.wA : u.wB);
-  const int col = (seg == 0 ? u.cA : u.cB) + c;
+  const bool in = 4 * lane < u.width;
+  const int col = u.col + 4 * lane;
   const float* base = reinterpret_cast<const float*>(u.W) + col;
   float acc[N][4] = {};
-  constexpr int kBatch = 8;  // rows in flight
-  for (int r0 = u.k0; r0 < u.k1; r0 += 32) {
-    const int n = min(32, u.k1 - r0);
+  constexpr int kBatch = 8;  // rows in flight, twice
+  struct Rows {
     float4 w[kBatch];
-    auto load = [&](int i0) {
+  };
+  const float* next = base + (size_t)u.k0 * u.ld;
+  int loaded = u.k0;
+  auto load = [&](Rows& s) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        w[i] = in && i0 + i < n ? __ldcs(reinterpret_cast<const float4*>(base + (size_t)(r0 + i0 + i) * u.ld))
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    load(0);
+    for (int i = 0; i < kBatch; ++i)
+      s.w[i] = in && loaded + i < u.k1 ? __ldcs(reinterpret_cast<const float4*>(next + (size_t)i * u.ld))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    next += (size_t)kBatch * u.ld;
+    loaded += kBatch;
+  };
+  auto multiply = [&](const Rows& s, int i0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int m = 0; m < N; ++m) {
+        const float v = coef[(i0 + i) * kGroup + m];
+        acc[m][0] = fmaf(v, s.w[i].x, acc[m][0]);
+        acc[m][1] = fmaf(v, s.w[i].y, acc[m][1]);
+        acc[m][2] = fmaf(v, s.w[i].z, acc[m][2]);
+        acc[m][3] = fmaf(v, s.w[i].w, acc[m][3]);
+      }
+  };
+  Rows s0, s1;
+  load(s0);
+  for (int r0 = u.k0; r0 < u.k1; r0 += 32) {
     __syncwarp();
 #pragma unroll
-    for (int m = 0; m < N; ++m)  // [row][token]
-      coef[lane * kGroup + m] = op[m] != nullptr && lane < n ? op[m][r0 + lane] : 0.f;
+    for (int m = 0; m < N; ++m)  // [row][token]; zero past the part
+      coef[lane * kGroup + m] = op[m] != nullptr && r0 + lane < u.k1 ? op[m][r0 + lane] : 0.f;
     __syncwarp();
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-      if (i0 > 0) load(i0);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int m = 0; m < N; ++m) {
-          const float v = coef[(i0 + i) * kGroup + m];
-          acc[m][0] = fmaf(v, w[i].x, acc[m][0]);
-          acc[m][1] = fmaf(v, w[i].y, acc[m][1]);
-          acc[m][2] = fmaf(v, w[i].z, acc[m][2]);
-          acc[m][3] = fmaf(v, w[i].w, acc[m][3]);
-        }
+    for (int i0 = 0; i0 < 32; i0 += 2 * kBatch) {
+      if (r0 + i0 >= u.k1) break;
+      load(s1);
+      multiply(s0, i0);
+      load(s0);
+      multiply(s1, i0 + kBatch);
     }
   }
 #pragma unroll
@@ -559,7 +570,7 @@ __device__ __forceinline__ void product_mx4(const Unit& u, const __half* op, con
   const int g = lane >> 2, t = lane & 3;
   const int first = u.k0 / 32, blocks = (u.k1 - u.k0) / 32;
   mx4::BlockCopies copies;
-  copies.start(u.W, u.scales, u.ld, u.cA, u.wA, first, 1, lane);
+  copies.start(u.W, u.scales, u.ld, u.col, u.width, first, 1, lane);
   struct Ops {
     uint2 b[2][2];  // [step][piece]; up to four tokens: [step][0]
     float s[2];
@@ -618,10 +629,10 @@ __device__ __forceinline__ void product_mx4(const Unit& u, const __half* op, con
     cur = next;
   }
   mx4::copies_wait<0>();
-  if (16 * g >= u.wA) return;
+  if (16 * g >= u.width) return;
 #pragma unroll
   for (int c = 0; c < 16; c += 4) {
-    const int col = u.cA + 16 * g + c;
+    const int col = u.col + 16 * g + c;
     if constexpr (kEight) {
       const float2 v[4] = {mx4::unpack2(acc8[0][c]), mx4::unpack2(acc8[0][c + 1]), mx4::unpack2(acc8[0][c + 2]),
                            mx4::unpack2(acc8[0][c + 3])};
@@ -730,30 +741,57 @@ struct Line {
   long long total;
   int shares;
 
-  __host__ __device__ Line(int units, int steps_, int workers) : steps(steps_), total((long long)units * steps_) {
-    const long long n = total / kMinShare;
-    shares = n < 1 ? 1 : n < workers ? (int)n : workers;
+  // rounds: shares per warp, where they keep eight steps each.
+  __host__ __device__ Line(int units, int steps_, int workers, int rounds)
+      : steps(steps_), total((long long)units * steps_) {
+    const long long n = total / kMinShare, longer = total / 8;
+    if (n <= workers)
+      shares = n < 1 ? 1 : (int)n;
+    else
+      shares = longer <= workers ? workers : longer < (long long)rounds * workers ? (int)longer : rounds * workers;
   }
-  // First step of a share; 32-bit division where the numbers allow it (a
-  // 64-bit one takes some hundred instructions).
-  __device__ __forceinline__ long long begin(int share) const {
-    const long long n = total * share;
-    return n >> 32 == 0 ? (long long)((unsigned)n / (unsigned)shares) : n / shares;
+  // n / c; 32-bit division where the numbers allow it (a 64-bit one takes some
+  // hundred instructions).
+  static __device__ __forceinline__ long long div(long long n, long long c) {
+    return n >> 32 == 0 ? (long long)((unsigned)n / (unsigned)c) : n / c;
   }
-  // The share that holds step `at`.
-  __device__ __forceinline__ int owner(long long at) const {
-    const long long n = (at + 1) * shares - 1;
-    return n >> 32 == 0 ? (int)((unsigned)n / (unsigned)total) : (int)(n / total);
-  }
-  __device__ __forceinline__ int unit(long long at) const {
-    return at >> 32 == 0 ? (int)((unsigned)at / (unsigned)steps) : (int)(at / steps);
-  }
+  // First step of a share, and the share that holds a step.
+  __device__ __forceinline__ long long begin(int share) const { return div(total * share, shares); }
+  __device__ __forceinline__ int owner(long long at) const { return (int)div((at + 1) * shares - 1, total); }
+  __device__ __forceinline__ int unit(long long at) const { return (int)div(at, steps); }
   // Shares that unit u's steps lie in: first, and how many.
   __device__ __forceinline__ int first(int u) const { return owner((long long)u * steps); }
   __device__ __forceinline__ int parts(int u) const { return owner((long long)(u + 1) * steps - 1) - first(u) + 1; }
   // The most parts a unit can have.
   int most_parts() const { return (int)((steps + total / shares - 1) / (total / shares)) + 1; }
 };
+
+// The next share of a warp beyond its first: asked for before the present one
+// is worked on (lane 0 holds the answer until then).
+__device__ __forceinline__ unsigned ask_share(unsigned* taken) {
+  return (threadIdx.x & 31) == 0 ? atomicAdd(taken, 1u) : 0u;
+}
+
+// Sums of `n` and `m` parts, `step` floats apart, in order.
+__device__ __forceinline__ void add_parts2(const float* a, int n, const float* b, int m, size_t step, float* sa,
+                                           float* sb) {
+  float x = 0.f, y = 0.f;
+  for (int i0 = 0; i0 < max(n, m); i0 += 8) {
+    float u[8], v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = i0 + i < n ? __ldcg(a + (size_t)(i0 + i) * step) : 0.f;
+      v[i] = i0 + i < m ? __ldcg(b + (size_t)(i0 + i) * step) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x += u[i];
+      y += v[i];
+    }
+  }
+  *sa = x;
+  *sb = y;
+}
 
 // Sum of `n` parts, `step` floats apart, in order.
 __device__ __forceinline__ float add_parts(const float* from, size_t step, int n) {
@@ -776,8 +814,7 @@ __device__ __forceinline__ size_t row_bytes_of(int cols) {
 // The down rows that a share starts with, on their way to L2.
 template <Fmt F>
 __device__ __forceinline__ void prefetch_rows(const Unit& u, int lane) {
-  const size_t row = row_bytes_of<F>(u.ld), c0 = row_bytes_of<F>(u.cA);
-  const size_t width = row_bytes_of<F>(u.wA + u.wB);
+  const size_t row = row_bytes_of<F>(u.ld), c0 = row_bytes_of<F>(u.col), width = row_bytes_of<F>(u.width);
   const int lines = (int)((width + 127) / 128);
   for (int i = lane; i < (u.k1 - u.k0) * lines; i += 32) {
     const uint8_t* from = u.W + (size_t)(u.k0 + i / lines) * row + c0 + min((size_t)(i % lines) * 128, width - 1);
@@ -835,40 +872,40 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   const int G = r.groups;
 
   // ------------------------------------------------------------------ gate | up
-  // units: tile, group and, MX4, half (gate, up), the last fastest
-  constexpr int kTile1 = F == Fmt::MX4 ? 128 : 64, kHalves = F == Fmt::MX4 ? 2 : 1;
-  const Line up(G * kHalves * ((p.f + kTile1 - 1) / kTile1), (p.d + kStep - 1) / kStep, workers);
+  // units: tile, group and half (gate, up), the last fastest
+  const Line up(G * 2 * ((p.f + 127) / 128), (p.d + kStep - 1) / kStep, workers, Cfg<F>::kRounds);
   const size_t up_slab = (size_t)pairs * 2 * p.f;
-  if (me < up.shares) {
+  for (int share = me; share < up.shares;) {
+    const unsigned next = ask_share(p.sync + kTaken1);
     const size_t expert_bytes = row_bytes_of<F>(2 * p.f) * p.d;
-    const long long stop = up.begin(me + 1);
-    for (long long at = up.begin(me); at < stop;) {
+    const long long stop = up.begin(share + 1);
+    for (long long at = up.begin(share); at < stop;) {
       const int w = up.unit(at), s0 = (int)(at - (long long)w * up.steps);
       const int s1 = (int)min((long long)up.steps, s0 + (stop - at));
-      const int group = w / kHalves % G, tile = w / kHalves / G, half = w % kHalves;
+      const int group = w / 2 % G, tile = w / 2 / G, half = w % 2;
       const int e = r.g_expert[group];
       Unit u;
       u.W = p.gu + (size_t)e * expert_bytes;
       u.scales = F == Fmt::MX4 ? p.gus + (size_t)e * (p.d / 32) * (2 * p.f) : nullptr;
       u.rows = p.d;
       u.ld = 2 * p.f;
-      u.cA = tile * kTile1 + half * p.f;
-      u.cB = p.f + tile * kTile1;
-      u.wA = min(kTile1, p.f - tile * kTile1);
-      u.wB = F == Fmt::MX4 ? 0 : u.wA;
+      u.col = tile * 128 + half * p.f;
+      u.width = min(128, p.f - tile * 128);
       u.n = r.g_n[group];
       u.k0 = s0 * kStep;
       u.k1 = min(p.d, s1 * kStep);
-      part_product<F, false>(p, &r, group, u, p.part1 + (size_t)(me - up.first(w)) * up_slab, 2 * p.f, smem);
+      part_product<F, false>(p, &r, group, u, p.part1 + (size_t)(share - up.first(w)) * up_slab, 2 * p.f, smem);
       at += s1 - s0;
     }
+    share = workers + (int)__shfl_sync(0xffffffffu, next, 0);
   }
 
   // ------------------------------------------------------------------ down
-  const Line down(G * ((p.d + 127) / 128), (p.f + kStep - 1) / kStep, workers);
+  const Line down(G * ((p.d + 127) / 128), (p.f + kStep - 1) / kStep, workers, Cfg<F>::kRounds);
   const size_t down_slab = (size_t)pairs * p.d;
-  long long at = me < down.shares ? down.begin(me) : 0;
-  const long long stop = me < down.shares ? down.begin(me + 1) : 0;
+  int share = me;
+  long long at = share < down.shares ? down.begin(share) : 0;
+  long long stop = share < down.shares ? down.begin(share + 1) : 0;
   const size_t expert_bytes = row_bytes_of<F>(p.d) * p.f;
   // this share's part of the unit at step `at`
   auto make_unit = [&](int* w, int* s1) {
@@ -882,10 +919,8 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
     u.scales = F == Fmt::MX4 ? p.dns + (size_t)e * (p.f / 32) * p.d : nullptr;
     u.rows = p.f;
     u.ld = p.d;
-    u.cA = tile * 128;
-    u.cB = u.cA + 64;
-    u.wA = F == Fmt::MX4 ? min(128, p.d - u.cA) : min(64, p.d - u.cA);
-    u.wB = F == Fmt::MX4 ? 0 : max(0, min(64, p.d - u.cB));
+    u.col = tile * 128;
+    u.width = min(128, p.d - u.col);
     u.n = r.g_n[group];
     u.k0 = s0 * kStep;
     u.k1 = min(p.f, *s1 * kStep);
@@ -899,22 +934,30 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
     const int chunks = (p.f + 31) / 32;
     for (int i = me; i < pairs * chunks; i += workers) {
       const int q = i / chunks, j = i % chunks * 32 + lane;
-      const int unit = (j / kTile1 * G + r.group_of[q]) * kHalves;
+      const int unit = (j / 128 * G + r.group_of[q]) * 2;
       const float* from = p.part1 + (size_t)q * 2 * p.f + j;
       // MX4: f is a multiple of 32, every lane has a column
       if (j < p.f) {
-        const int n = up.parts(unit);
-        const float g = add_parts(from, up_slab, n);
-        const float v = add_parts(from + p.f, up_slab, kHalves == 2 ? up.parts(unit + 1) : n);
+        const int n = up.parts(unit), m = up.parts(unit + 1);
+        float g, v;
+        add_parts2(from, n, from + p.f, m, up_slab, &g, &v);
         put_h<F>(p, q, j, g, v, lane);
       }
     }
   }
   if (!grid_barrier(p.sync + 2, &r, p)) return;
-  while (at < stop) {
-    const Unit u = make_unit(&w, &s1);
-    part_product<F, true>(p, &r, w % G, u, p.part2 + (size_t)(me - down.first(w)) * down_slab, p.d, smem);
-    at = (long long)w * down.steps + s1;
+  while (share < down.shares) {
+    const unsigned next = ask_share(p.sync + kTaken2);
+    while (at < stop) {
+      const Unit u = make_unit(&w, &s1);
+      part_product<F, true>(p, &r, w % G, u, p.part2 + (size_t)(share - down.first(w)) * down_slab, p.d, smem);
+      at = (long long)w * down.steps + s1;
+    }
+    share = workers + (int)__shfl_sync(0xffffffffu, next, 0);
+    if (share < down.shares) {
+      at = down.begin(share);
+      stop = down.begin(share + 1);
+    }
   }
   if (!grid_barrier(p.sync + 3, &r, p)) return;
 
@@ -950,7 +993,7 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   // the barriers' words are zero again once every CTA has passed the last one
   if (tid == 0 && atomic_add_acq_rel_gpu(p.sync + kSyncEnd, 1u) == gridDim.x - 1u) {
 #pragma unroll
-    for (int i = 0; i <= kBarriers; ++i) p.sync[i] = 0u;
+    for (int i = 0; i < kSyncWords; ++i) p.sync[i] = 0u;
   }
 }
 
@@ -960,15 +1003,14 @@ struct MoePlan {
 
 MoePlan make_plan(int M, int d, int f, int E, int k, MoeFormat fmt) {
   MoePlan pl;
-  const bool mx4 = fmt == MoeFormat::MX4;
-  const int step = fmt == MoeFormat::BF16 ? 16 : 32;
+  const int rounds = fmt == MoeFormat::MX4 ? Cfg<Fmt::MX4>::kRounds : Cfg<Fmt::BF16>::kRounds;
+  const int step = fmt == MoeFormat::BF16 ? 16 : fmt == MoeFormat::F32 ? 8 : 32;
   const int workers = 148 * kCtasPerSm * kWarps;
   // A unit has the most parts where there are the fewest units: there are at
   // least k groups (a token's experts differ) and one for every eight pairs.
   const int groups = std::max(k, (M * k + kGroup - 1) / kGroup);
-  const int units1 = groups * (mx4 ? 2 * ((f + 127) / 128) : (f + 63) / 64);
-  const int parts1 = Line(units1, (d + step - 1) / step, workers).most_parts();
-  const int parts2 = Line(groups * ((d + 127) / 128), (f + step - 1) / step, workers).most_parts();
+  const int parts1 = Line(groups * 2 * ((f + 127) / 128), (d + step - 1) / step, workers, rounds).most_parts();
+  const int parts2 = Line(groups * ((d + 127) / 128), (f + step - 1) / step, workers, rounds).most_parts();
   const size_t pairs = (size_t)M * k;
   size_t off = 0;
   auto take = [&](size_t bytes) {
