@@ -97,8 +97,15 @@ struct Routing {
   double sums[kWarps][4];  // scores: the warps' shares
   float gate[kMaxPairs];
   int expert[kMaxPairs];
-  int cnt[kMaxE];
-  int base[kMaxE];
+  double score[kMaxPairs];  // of the chosen experts
+  union {
+    struct {
+      int cnt[kMaxE];
+      int base[kMaxE];
+    };
+    unsigned long long key[kMaxE];  // selection by rank
+  };
+  int rank[kMaxE];
   short g_expert[kMaxPairs];
   short g_n[kMaxPairs];
   short g_pair[kMaxPairs][kGroup];
@@ -235,6 +242,29 @@ __device__ __forceinline__ double key_score(unsigned long long k) {
   return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
 
+// Token m's experts and gates: lane s < k of a whole warp holds the s-th
+// expert and its score; den: the sum of every expert's exponential, taken
+// where the gates are not renormalised.
+__device__ __forceinline__ void write_gates(const MParams& p, Routing* r, int m, int expert, double score, float den) {
+  const int lane = threadIdx.x & 31;
+  const double top = __shfl_sync(0xffffffffu, score, 0);
+  const float mine = lane < p.k ? expf((float)(score - top)) : 0.f;
+  if (p.renormalize) {
+    den = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  }
+  if (lane < p.k) {
+    const int q = m * p.k + lane;
+    r->expert[q] = expert;
+    r->gate[q] = mine / den;
+    if (blockIdx.x == 0) {
+      if (p.idx != nullptr) p.idx[q] = expert;
+      if (p.gate != nullptr) p.gate[q] = mine / den;
+    }
+  }
+}
+
 // Selection and softmax of token m by one warp; a lane holds kPer scores.
 template <int kPer>
 __device__ void route_token(const MParams& p, Routing* r, int m) {
@@ -253,8 +283,8 @@ __device__ void route_token(const MParams& p, Routing* r, int m) {
     }
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) report(p.dev_status, LAROSA_DEV_NONFINITE);
-  float den = 0.f, mine = 0.f;    // lane s: exp of the s-th score's distance from the first
-  int expert = 0;
+  float den = 0.f;
+  int expert = 0;  // lane s: the s-th
   if (!p.renormalize) {
     // the sum over every expert, before keys are taken out
     unsigned long long best = 0ull;
@@ -301,22 +331,63 @@ __device__ void route_token(const MParams& p, Routing* r, int m) {
       expert = (int)e;
     }
   }
-  const double l0 = __shfl_sync(0xffffffffu, score, 0);
-  mine = lane < p.k ? expf((float)(score - l0)) : 0.f;
-  if (p.renormalize) {
-    den = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  write_gates(p, r, m, expert, score, den);
+}
+
+// Selection by the CTA for few scores in all (at most kMaxE): an expert's rank
+// is the number of its token's experts that come before it.  One pass of
+// comparisons spread over all threads, where a warp's k rounds of searching
+// for the largest take about 500 clocks each (a layer of 128 experts of 2048
+// to 768, one token, k = 8: 43.9 us with the rounds, 43.3 so; 8 experts of 256
+// to 512, k = 2: 18.0 and 19.1).
+__device__ void route_by_rank(const MParams& p, Routing* r) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int items = p.M * p.E;
+  bool bad = false;
+  for (int i = tid; i < items; i += kT) {
+    const double v = __ldcg(p.logits + i);
+    r->key[i] = score_key(v);
+    r->rank[i] = 0;
+    bad |= !isfinite(v);
   }
-  if (lane < p.k) {
-    const int q = m * p.k + lane;
-    r->expert[q] = expert;
-    r->gate[q] = mine / den;
-    if (blockIdx.x == 0) {
-      if (p.idx != nullptr) p.idx[q] = expert;
-      if (p.gate != nullptr) p.gate[q] = mine / den;
+  if (__syncthreads_or(bad) && tid == 0 && blockIdx.x == 0) report(p.dev_status, LAROSA_DEV_NONFINITE);
+  // `share` threads per item, each an equal range of the others
+  int share = 1;
+  while (items * share * 2 <= kT) share *= 2;
+  for (int i = tid; i < items * share; i += kT) {
+    const int item = i / share, e = item % p.E;
+    const unsigned long long* row = r->key + item - e;
+    const unsigned long long mine = row[e];
+    const int from = i % share * p.E / share, to = (i % share + 1) * p.E / share;
+    int before = 0;
+    for (int o = from; o < to; ++o) before += row[o] > mine || (row[o] == mine && o < e);
+    if (share == 1)
+      r->rank[item] = before;
+    else
+      atomicAdd(&r->rank[item], before);
+  }
+  __syncthreads();
+  for (int i = tid; i < items; i += kT) {
+    const int rank = r->rank[i], m = i / p.E;
+    if (rank < p.k) {
+      r->expert[m * p.k + rank] = i % p.E;
+      r->score[m * p.k + rank] = key_score(r->key[i]);
     }
   }
+  __syncthreads();
+  for (int m = warp; m < p.M; m += kWarps) {
+    const int expert = lane < p.k ? r->expert[m * p.k + lane] : 0;
+    const double score = lane < p.k ? r->score[m * p.k + lane] : 0.0;
+    float den = 0.f;
+    if (!p.renormalize) {
+      const double top = __shfl_sync(0xffffffffu, score, 0);
+      for (int e = lane; e < p.E; e += 32) den += expf((float)(key_score(r->key[m * p.E + e]) - top));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    }
+    write_gates(p, r, m, expert, score, den);
+  }
+  __syncthreads();  // the keys are used up
 }
 
 // The groups of up to 32 pairs (token, slot), by one warp: experts in the
@@ -506,7 +577,7 @@ __device__ __forceinline__ void product_f32(const Unit& u, const float* const (&
   const int col = u.col + 4 * lane;
   const float* base = reinterpret_cast<const float*>(u.W) + col;
   float acc[N][4] = {};
-  constexpr int kBatch = 8;  // rows in flight, twice
+  constexpr int kBatch = N == 8 ? 4 : 8;  // rows in flight, twice: more spill at eight tokens
   struct Rows {
     float4 w[kBatch];
   };
@@ -776,15 +847,15 @@ __device__ __forceinline__ unsigned ask_share(unsigned* taken) {
 __device__ __forceinline__ void add_parts2(const float* a, int n, const float* b, int m, size_t step, float* sa,
                                            float* sb) {
   float x = 0.f, y = 0.f;
-  for (int i0 = 0; i0 < max(n, m); i0 += 8) {
-    float u[8], v[8];
+  for (int i0 = 0; i0 < max(n, m); i0 += 16) {
+    float u[16], v[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       u[i] = i0 + i < n ? __ldcg(a + (size_t)(i0 + i) * step) : 0.f;
       v[i] = i0 + i < m ? __ldcg(b + (size_t)(i0 + i) * step) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       x += u[i];
       y += v[i];
     }
@@ -854,15 +925,19 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   if (!grid_barrier(p.sync, &r, p)) return;
 
   // ------------------------------------------------------------------ routing
-  for (int m = warp; m < p.M; m += kWarps) {
-    if (p.E <= 32)
-      route_token<1>(p, &r, m);
-    else if (p.E <= 128)
-      route_token<4>(p, &r, m);
-    else
-      route_token<kMaxE / 32>(p, &r, m);
+  if (p.k >= 4 && p.E <= 128 && p.M * p.E <= kMaxE) {
+    route_by_rank(p, &r);
+  } else {
+    for (int m = warp; m < p.M; m += kWarps) {
+      if (p.E <= 32)
+        route_token<1>(p, &r, m);
+      else if (p.E <= 128)
+        route_token<4>(p, &r, m);
+      else
+        route_token<kMaxE / 32>(p, &r, m);
+    }
+    __syncthreads();
   }
-  __syncthreads();
   if (pairs <= 32) {
     if (warp == 0) build_groups_warp(p, &r);
     __syncthreads();
