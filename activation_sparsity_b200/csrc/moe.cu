@@ -94,10 +94,20 @@ struct MParams {
 
 // The routing of a call, the same in every CTA.
 struct Routing {
-  double sums[kWarps][4];  // scores: the warps' shares
   float gate[kMaxPairs];
   int expert[kMaxPairs];
-  double score[kMaxPairs];  // of the chosen experts
+  short g_expert[kMaxPairs];
+  short g_n[kMaxPairs];
+  uint8_t g_pair[kMaxPairs][kGroup];
+  short group_of[kMaxPairs];
+  int groups;
+  int ok;
+};
+static_assert(kMaxPairs <= 256, "a pair's number is a byte");
+
+// What the phases without products work in; lies where the products keep
+// their rows.
+struct Scratch {
   union {
     struct {
       int cnt[kMaxE];
@@ -106,13 +116,9 @@ struct Routing {
     unsigned long long key[kMaxE];  // selection by rank
   };
   int rank[kMaxE];
-  short g_expert[kMaxPairs];
-  short g_n[kMaxPairs];
-  short g_pair[kMaxPairs][kGroup];
-  short group_of[kMaxPairs];
-  float join[kWarps][32];  // y: the experts' sums
-  int groups;
-  int ok;
+  double score[kMaxPairs];  // of the chosen experts
+  double sums[kWarps][4];   // scores: the warps' shares
+  float join[kWarps][32];   // y: the experts' sums
 };
 
 // ---------------------------------------------------------------- grid-wide barrier
@@ -169,7 +175,7 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
 
 // Tasks (expert, four tokens), one CTA each.
 template <typename T>
-__device__ void scores(const MParams& p, Routing* r) {
+__device__ void scores(const MParams& p, Scratch* r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tg = (p.M + 3) / 4;
   const T* x = static_cast<const T*>(p.x);
@@ -212,16 +218,16 @@ __device__ void scores(const MParams& p, Routing* r) {
 }
 
 // v of row `lane` of block `b` of token (or pair) m as MX4 pieces: op holds
-// [count][2][n] f16, then [count][n / 32] scales.
+// [count][n / 32][2][32] f16, then [count][n / 32] scales.
 __device__ __forceinline__ void put_pieces(unsigned char* op, int count, int n, int m, int b, float v, int lane) {
   const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
   float up, down;
   mx4::piece_scale(top, &up, &down);
   __half p0, p1;
   mx4::split_pieces(v * up, &p0, &p1);
-  __half* row = reinterpret_cast<__half*>(op) + (size_t)m * 2 * n + b * 32 + lane;
+  __half* row = reinterpret_cast<__half*>(op) + (size_t)m * 2 * n + b * 64 + lane;
   row[0] = p0;
-  row[n] = p1;
+  row[32] = p1;
   if (lane == 0) reinterpret_cast<float*>(op + (size_t)count * 4 * n)[(size_t)m * (n / 32) + b] = down;
 }
 
@@ -340,14 +346,14 @@ __device__ void route_token(const MParams& p, Routing* r, int m) {
 // for the largest take about 500 clocks each (a layer of 128 experts of 2048
 // to 768, one token, k = 8: 43.9 us with the rounds, 43.3 so; 8 experts of 256
 // to 512, k = 2: 18.0 and 19.1).
-__device__ void route_by_rank(const MParams& p, Routing* r) {
+__device__ void route_by_rank(const MParams& p, Routing* r, Scratch* w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = p.M * p.E;
   bool bad = false;
   for (int i = tid; i < items; i += kT) {
     const double v = __ldcg(p.logits + i);
-    r->key[i] = score_key(v);
-    r->rank[i] = 0;
+    w->key[i] = score_key(v);
+    w->rank[i] = 0;
     bad |= !isfinite(v);
   }
   if (__syncthreads_or(bad) && tid == 0 && blockIdx.x == 0) report(p.dev_status, LAROSA_DEV_NONFINITE);
@@ -356,32 +362,32 @@ __device__ void route_by_rank(const MParams& p, Routing* r) {
   while (items * share * 2 <= kT) share *= 2;
   for (int i = tid; i < items * share; i += kT) {
     const int item = i / share, e = item % p.E;
-    const unsigned long long* row = r->key + item - e;
+    const unsigned long long* row = w->key + item - e;
     const unsigned long long mine = row[e];
     const int from = i % share * p.E / share, to = (i % share + 1) * p.E / share;
     int before = 0;
     for (int o = from; o < to; ++o) before += row[o] > mine || (row[o] == mine && o < e);
     if (share == 1)
-      r->rank[item] = before;
+      w->rank[item] = before;
     else
-      atomicAdd(&r->rank[item], before);
+      atomicAdd(&w->rank[item], before);
   }
   __syncthreads();
   for (int i = tid; i < items; i += kT) {
-    const int rank = r->rank[i], m = i / p.E;
+    const int rank = w->rank[i], m = i / p.E;
     if (rank < p.k) {
       r->expert[m * p.k + rank] = i % p.E;
-      r->score[m * p.k + rank] = key_score(r->key[i]);
+      w->score[m * p.k + rank] = key_score(w->key[i]);
     }
   }
   __syncthreads();
   for (int m = warp; m < p.M; m += kWarps) {
     const int expert = lane < p.k ? r->expert[m * p.k + lane] : 0;
-    const double score = lane < p.k ? r->score[m * p.k + lane] : 0.0;
+    const double score = lane < p.k ? w->score[m * p.k + lane] : 0.0;
     float den = 0.f;
     if (!p.renormalize) {
       const double top = __shfl_sync(0xffffffffu, score, 0);
-      for (int e = lane; e < p.E; e += 32) den += expf((float)(key_score(r->key[m * p.E + e]) - top));
+      for (int e = lane; e < p.E; e += 32) den += expf((float)(key_score(w->key[m * p.E + e]) - top));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     }
@@ -409,7 +415,7 @@ __device__ void build_groups_warp(const MParams& p, Routing* r) {
   const int base = __shfl_sync(0xffffffffu, incl - n, __ffs(same) - 1);
   if (lane < pairs) {
     const int g = base + rank / kGroup;
-    r->g_pair[g][rank % kGroup] = (short)lane;
+    r->g_pair[g][rank % kGroup] = (uint8_t)lane;
     r->group_of[lane] = (short)g;
     if (rank % kGroup == 0) {
       r->g_expert[g] = (short)e;
@@ -420,25 +426,25 @@ __device__ void build_groups_warp(const MParams& p, Routing* r) {
 }
 
 // The groups of more pairs, by the CTA: experts in ascending order.
-__device__ void build_groups(const MParams& p, Routing* r) {
+__device__ void build_groups(const MParams& p, Routing* r, Scratch* w) {
   const int tid = threadIdx.x;
   const int pairs = p.M * p.k;
-  for (int e = tid; e < p.E; e += kT) r->cnt[e] = 0;
+  for (int e = tid; e < p.E; e += kT) w->cnt[e] = 0;
   __syncthreads();
-  for (int q = tid; q < pairs; q += kT) atomicAdd(&r->cnt[r->expert[q]], 1);
+  for (int q = tid; q < pairs; q += kT) atomicAdd(&w->cnt[r->expert[q]], 1);
   __syncthreads();
   if (tid < 32) {
     int before = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + tid;
-      const int n = e < p.E ? (r->cnt[e] + kGroup - 1) / kGroup : 0;
+      const int n = e < p.E ? (w->cnt[e] + kGroup - 1) / kGroup : 0;
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (tid >= o) incl += v;
       }
-      if (e < p.E) r->base[e] = before + incl - n;
+      if (e < p.E) w->base[e] = before + incl - n;
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (tid == 0) r->groups = before;
@@ -448,12 +454,12 @@ __device__ void build_groups(const MParams& p, Routing* r) {
     const int e = r->expert[q];
     int rank = 0;
     for (int o = 0; o < q; ++o) rank += r->expert[o] == e;
-    const int g = r->base[e] + rank / kGroup;
-    r->g_pair[g][rank % kGroup] = (short)q;
+    const int g = w->base[e] + rank / kGroup;
+    r->g_pair[g][rank % kGroup] = (uint8_t)q;
     r->group_of[q] = (short)g;
     if (rank % kGroup == 0) {
       r->g_expert[g] = (short)e;
-      r->g_n[g] = (short)min(kGroup, r->cnt[e] - rank);
+      r->g_n[g] = (short)min(kGroup, w->cnt[e] - rank);
     }
   }
   __syncthreads();
@@ -472,16 +478,36 @@ struct Unit {
   int n;  // tokens
 };
 
+// MX4: a block of 32 rows by 128 columns and the operands of up to eight
+// tokens for it.  Token m's 16-byte chunk c (piece, step, half step) lies at
+// chunk c ^ 2 (m % 4): four tokens' reads of 32 bytes fall into different banks.
+struct __align__(16) Stage {
+  mx4::Tile tile;
+  __half op[kGroup][2][32];
+  float scale[kGroup];
+
+  __device__ __forceinline__ __half* chunk(int m, int c) { return &op[m][0][0] + 8 * (c ^ (2 * (m & 3))); }
+};
+
 template <Fmt F>
 struct Cfg {
   static constexpr int kStep = F == Fmt::BF16 ? 16 : F == Fmt::F32 ? 8 : 32;  // rows of a step
   static constexpr int kRounds = F == Fmt::MX4 ? 6 : 1;   // shares per warp
-  static constexpr int kRing = 4;                         // MX4: tiles of a warp's ring
+  static constexpr int kRing = 4;                         // MX4: stages of a warp's ring
   static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
                                       : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
-                                                      : kRing * sizeof(mx4::Tile);
-  static constexpr size_t kSmem = kWarps * kWarpSmem;
+                                                      : kRing * sizeof(Stage);
+  static constexpr size_t kSmem = std::max(kWarps * kWarpSmem, sizeof(Scratch));
 };
+
+// Asynchronous copies to shared memory of `bytes` (all or none) bytes; the rest
+// is filled with zeros.
+__device__ __forceinline__ void copy16_or_zero(void* dst, const void* src, unsigned bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4_or_zero(void* dst, const void* src, unsigned bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -626,43 +652,43 @@ __device__ __forceinline__ void product_f32(const Unit& u, const float* const (&
       __stcg(reinterpret_cast<float4*>(out[m] + col), make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]));
 }
 
-// MX4 weights: blocks of 32 rows through the warp's ring of tiles.
-//   kEight   op: pieces of the token in column g of B (token g), the second
-//            u.rows halves after the first; sx: block scales of the tokens 2 t
-//            and 2 t + 1, o: where their sums go
-//   else     up to four tokens; op: piece g % 2 of token g / 2; sx[0], o[0]: of
-//            token t
+// MX4 weights: blocks of 32 rows, with their operands, through the warp's ring
+// of stages.  mine: pieces and block scales of token lane / 4 of the group, its
+// first row's (null: no token).  B holds, in column g:
+//   kEight   one piece of token g; o: where the sums of 2 t and 2 t + 1 go
+//   else     piece g % 2 of token g / 2; o[0]: of token t
 // Null: no token.
 template <bool kEight>
-__device__ __forceinline__ void product_mx4(const Unit& u, const __half* op, const float* const (&sx)[2],
-                                            float* const (&o)[2], mx4::Tile* ring) {
+__device__ __forceinline__ void product_mx4(const Unit& u, const __half* mine, const float* mine_scales,
+                                            float* const (&o)[2], Stage* ring) {
   constexpr int kRing = Cfg<Fmt::MX4>::kRing;
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int first = u.k0 / 32, blocks = (u.k1 - u.k0) / 32;
   mx4::BlockCopies copies;
   copies.start(u.W, u.scales, u.ld, u.col, u.width, first, 1, lane);
-  struct Ops {
-    uint2 b[2][2];  // [step][piece]; up to four tokens: [step][0]
-    float s[2];
+  const unsigned present = mine != nullptr;
+  if (present) {
+    mine += first * 64 + 16 * t;
+    mine_scales += first;
+  } else {  // copies of no bytes: zeros
+    mine = reinterpret_cast<const __half*>(u.W);
+    mine_scales = reinterpret_cast<const float*>(u.W);
+  }
+  auto fetch = [&](Stage& st) {
+    copies.next(st.tile, lane);
+    if (kEight || g < 4) {
+      copy16_or_zero(st.chunk(g, 2 * t), mine, present * 16);
+      copy16_or_zero(st.chunk(g, 2 * t + 1), mine + 8, present * 16);
+      if (t == 0) copy4_or_zero(&st.scale[g], mine_scales, present * 4);
+    }
+    mine += present * 64;
+    mine_scales += present;
   };
-  const __half* op_at = op != nullptr ? op + first * 32 + 4 * t : nullptr;
-  auto load_ops = [&](int i, Ops& v) {
-    const bool in = i < blocks;
-#pragma unroll
-    for (int step = 0; step < 2; ++step)
-#pragma unroll
-      for (int piece = 0; piece < (kEight ? 2 : 1); ++piece)
-        v.b[step][piece] = in && op_at != nullptr ? *reinterpret_cast<const uint2*>(
-                                                        op_at + (size_t)piece * u.rows + i * 32 + 16 * step)
-                                                  : make_uint2(0u, 0u);
-#pragma unroll
-    for (int j = 0; j < (kEight ? 2 : 1); ++j) v.s[j] = in && sx[j] != nullptr ? sx[j][first + i] : 0.f;
-  };
-  __syncwarp();  // the part before has read its tiles
+  __syncwarp();  // the part before has read its stages
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) {
-    if (s < blocks) copies.next(ring[s], lane);
+    if (s < blocks) fetch(ring[s]);
     mx4::copies_commit();
   }
   unsigned long long acc8[1][16];
@@ -672,32 +698,32 @@ __device__ __forceinline__ void product_mx4(const Unit& u, const __half* op, con
     acc8[0][c] = 0ull;
     acc4[0][c / 2][c % 2] = 0.f;
   }
-  Ops cur;
-  load_ops(0, cur);
   int now = 0, fill = kRing - 1;
 #pragma unroll 1
   for (int i = 0; i < blocks; ++i) {
-    __syncwarp();  // every lane has read the tile that is filled next
-    if (i + kRing - 1 < blocks) copies.next(ring[fill], lane);
+    __syncwarp();  // every lane has read the stage that is filled next
+    if (i + kRing - 1 < blocks) fetch(ring[fill]);
     mx4::copies_commit();
-    Ops next;
-    load_ops(i + 1, next);
     mx4::copies_wait<kRing - 1>();
     __syncwarp();  // the other lanes' copies too
+    Stage& st = ring[now];
     mx4::RowSet rs;
-    rs.read<4, 4>(ring[now], g, t);
+    rs.read<4, 4>(st.tile, g, t);
     now = now + 1 == kRing ? 0 : now + 1;
     fill = fill + 1 == kRing ? 0 : fill + 1;
+    // the four halves of `step` that this lane multiplies, of a token's piece
+    auto operand = [&](int m, int piece, int step) {
+      return *reinterpret_cast<const uint2*>(st.chunk(m, 4 * piece + 2 * step + (t >> 1)) + 4 * (t & 1));
+    };
     if constexpr (kEight) {
-      const uint2 b[2][1][2] = {{{cur.b[0][0], cur.b[0][1]}}, {{cur.b[1][0], cur.b[1][1]}}};
-      const unsigned long long s2[1] = {mx4::pack2(cur.s[0], cur.s[1])};
+      const uint2 b[2][1][2] = {{{operand(g, 0, 0), operand(g, 1, 0)}}, {{operand(g, 0, 1), operand(g, 1, 1)}}};
+      const unsigned long long s2[1] = {*reinterpret_cast<const unsigned long long*>(&st.scale[2 * t])};
       mx4::block_product8<1>(rs, b, s2, acc8);
     } else {
-      const uint2 b[2][1] = {{cur.b[0][0]}, {cur.b[1][0]}};
-      const float s1[1] = {cur.s[0]};
+      const uint2 b[2][1] = {{operand(g >> 1, g & 1, 0)}, {operand(g >> 1, g & 1, 1)}};
+      const float s1[1] = {st.scale[t]};
       mx4::block_product<1, 4, 4>(rs, b, s1, acc4);
     }
-    cur = next;
   }
   mx4::copies_wait<0>();
   if (16 * g >= u.width) return;
@@ -766,21 +792,16 @@ __device__ __forceinline__ void part_product(const MParams& p, const Routing* r,
     const unsigned char* src = kDown ? p.hop : p.xop;
     const __half* pieces = reinterpret_cast<const __half*>(src);
     const float* scales = reinterpret_cast<const float*>(src + (size_t)(kDown ? p.M * p.k : p.M) * 4 * rows);
-    auto scales_of = [&](int pos) -> const float* {
-      const int o = operand(pos);
-      return o < 0 ? nullptr : scales + (size_t)o * (rows / 32);
-    };
-    mx4::Tile* ring = reinterpret_cast<mx4::Tile*>(smem + warp * Cfg<F>::kWarpSmem);
+    Stage* ring = reinterpret_cast<Stage*>(smem + warp * Cfg<F>::kWarpSmem);
+    const int o = operand(g);
+    const __half* mine = o < 0 ? nullptr : pieces + (size_t)o * 2 * rows;
+    const float* mine_scales = o < 0 ? nullptr : scales + (size_t)o * (rows / 32);
     if (u.n <= 4) {
-      const int o = operand(g >> 1);
-      const float* const sx[2] = {scales_of(t), nullptr};
       float* const to[2] = {sums_of(t), nullptr};
-      product_mx4<false>(u, o < 0 ? nullptr : pieces + ((size_t)o * 2 + (g & 1)) * rows, sx, to, ring);
+      product_mx4<false>(u, mine, mine_scales, to, ring);
     } else {
-      const int o = operand(g);
-      const float* const sx[2] = {scales_of(2 * t), scales_of(2 * t + 1)};
       float* const to[2] = {sums_of(2 * t), sums_of(2 * t + 1)};
-      product_mx4<true>(u, o < 0 ? nullptr : pieces + (size_t)o * 2 * rows, sx, to, ring);
+      product_mx4<true>(u, mine, mine_scales, to, ring);
     }
   }
 }
@@ -903,15 +924,16 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   // shares are dealt over the CTAs first, so that few of them land on many SMs
   const int me = warp * gridDim.x + blockIdx.x, workers = kWarps * gridDim.x;
 
+  Scratch& work = *reinterpret_cast<Scratch*>(smem);
   pdl_wait();
   pdl_launch_dependents();
 
   // ------------------------------------------------------------------ scores
   const bool x_f32 = F == Fmt::F32 || (F == Fmt::MX4 && p.x_f32);
   if (x_f32)
-    scores<float>(p, &r);
+    scores<float>(p, &work);
   else
-    scores<__nv_bfloat16>(p, &r);
+    scores<__nv_bfloat16>(p, &work);
   if constexpr (F == Fmt::MX4) {
     const int blocks = p.d / 32;
     for (int i = me; i < p.M * blocks; i += workers) {
@@ -926,7 +948,7 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
 
   // ------------------------------------------------------------------ routing
   if (p.k >= 4 && p.E <= 128 && p.M * p.E <= kMaxE) {
-    route_by_rank(p, &r);
+    route_by_rank(p, &r, &work);
   } else {
     for (int m = warp; m < p.M; m += kWarps) {
       if (p.E <= 32)
@@ -942,7 +964,7 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
     if (warp == 0) build_groups_warp(p, &r);
     __syncthreads();
   } else {
-    build_groups(p, &r);
+    build_groups(p, &r, &work);
   }
   const int G = r.groups;
 
@@ -1055,10 +1077,10 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
           const int q = m * p.k + s;
           v = add_parts(p.part2 + (size_t)q * p.d + c, down_slab, down.parts(c / 128 * G + r.group_of[q]));
         }
-        r.join[warp][lane] = v;
+        work.join[warp][lane] = v;
         __syncthreads();
         if (i_team == 0 && in)
-          for (int i = 0; i < team && s0 + i < p.k; ++i) y = fmaf(r.gate[m * p.k + s0 + i], r.join[warp + i][lane], y);
+          for (int i = 0; i < team && s0 + i < p.k; ++i) y = fmaf(r.gate[m * p.k + s0 + i], work.join[warp + i][lane], y);
         __syncthreads();
       }
       if (i_team == 0 && in) p.y[(size_t)m * p.d + c] = y;
