@@ -118,7 +118,7 @@ struct Scratch {
   int rank[kMaxE];
   double score[kMaxPairs];  // of the chosen experts
   double sums[kWarps][4];   // scores: the warps' shares
-  float join[kWarps][32];   // y: the experts' sums
+  float4 join[kWarps][32];  // the warps' shares of a sum of parts
 };
 
 // ---------------------------------------------------------------- grid-wide barrier
@@ -806,23 +806,46 @@ __device__ __forceinline__ void part_product(const MParams& p, const Routing* r,
   }
 }
 
-// h of pair q, column j: stored as the operand of the down product.  Lanes of
-// a warp hold neighbouring columns.
+// h of pair q, columns j .. j + 3 (in: there are such): stored as the operand of
+// the down product.  Eight neighbouring lanes hold a block of 32.
 template <Fmt F>
-__device__ __forceinline__ void put_h(const MParams& p, int q, int j, float g, float u, int lane) {
-  const float h = g / (1.f + expf(-g)) * u;
+__device__ __forceinline__ void put_h(const MParams& p, int q, int j, float4 g, float4 u, bool in) {
+  const float a[4] = {g.x, g.y, g.z, g.w}, b[4] = {u.x, u.y, u.z, u.w};
+  float h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = a[i] / (1.f + expf(-a[i])) * b[i];
   if constexpr (F == Fmt::BF16) {
+    if (!in) return;
     __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(p.hop) + (size_t)q * 3 * p.f + j;
-    const __nv_bfloat16 a = __float2bfloat16_rn(h);
-    const float r1 = h - __bfloat162float(a);
-    const __nv_bfloat16 b = __float2bfloat16_rn(r1);
-    at[0] = a;
-    at[p.f] = b;
-    at[2 * p.f] = __float2bfloat16_rn(r1 - __bfloat162float(b));
+#pragma unroll
+    for (int piece = 0; piece < 3; ++piece) {
+      __align__(8) __nv_bfloat16 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __float2bfloat16_rn(h[i]);
+        h[i] -= __bfloat162float(v[i]);
+      }
+      *reinterpret_cast<uint2*>(at + (size_t)piece * p.f) = *reinterpret_cast<const uint2*>(v);
+    }
   } else if constexpr (F == Fmt::F32) {
-    reinterpret_cast<float*>(p.hop)[(size_t)q * p.f + j] = h;
+    if (in) *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.hop) + (size_t)q * p.f + j) = make_float4(h[0], h[1], h[2], h[3]);
   } else {
-    put_pieces(p.hop, p.M * p.k, p.f, q, j / 32, h, lane);
+    unsigned top = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(h[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (!in) return;  // f is a multiple of 32: whole blocks
+    float up, down;
+    mx4::piece_scale(top, &up, &down);
+    __align__(8) __half v0[4], v1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx4::split_pieces(h[i] * up, &v0[i], &v1[i]);
+    __half* at = reinterpret_cast<__half*>(p.hop) + (size_t)q * 2 * p.f + j / 32 * 64 + j % 32;
+    *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(v0);
+    *reinterpret_cast<uint2*>(at + 32) = *reinterpret_cast<const uint2*>(v1);
+    if (j % 32 == 0)
+      reinterpret_cast<float*>(p.hop + (size_t)p.M * p.k * 4 * p.f)[(size_t)q * (p.f / 32) + j / 32] = down;
   }
 }
 
@@ -864,36 +887,21 @@ __device__ __forceinline__ unsigned ask_share(unsigned* taken) {
   return (threadIdx.x & 31) == 0 ? atomicAdd(taken, 1u) : 0u;
 }
 
-// Sums of `n` and `m` parts, `step` floats apart, in order.
-__device__ __forceinline__ void add_parts2(const float* a, int n, const float* b, int m, size_t step, float* sa,
-                                           float* sb) {
-  float x = 0.f, y = 0.f;
-  for (int i0 = 0; i0 < max(n, m); i0 += 16) {
-    float u[16], v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      u[i] = i0 + i < n ? __ldcg(a + (size_t)(i0 + i) * step) : 0.f;
-      v[i] = i0 + i < m ? __ldcg(b + (size_t)(i0 + i) * step) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      x += u[i];
-      y += v[i];
-    }
-  }
-  *sa = x;
-  *sb = y;
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// Sum of `n` parts, `step` floats apart, in order.
-__device__ __forceinline__ float add_parts(const float* from, size_t step, int n) {
-  float s = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 16) {
-    float v[16];
+// Sum of four columns' parts [i0, i1), `step` floats apart, in order.
+__device__ __forceinline__ float4 add_parts(const float* from, size_t step, int i0, int i1) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  from += (size_t)i0 * step;
+  for (int i = i0; i < i1; i += 8, from += 8 * step) {
+    float4 v[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i0 + i < n ? __ldcg(from + (size_t)(i0 + i) * step) : 0.f;
+    for (int j = 0; j < 8; ++j)
+      v[j] = i + j < i1 ? __ldcg(reinterpret_cast<const float4*>(from + (size_t)j * step)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += v[i];
+    for (int j = 0; j < 8; ++j) s = add4(s, v[j]);
   }
   return s;
 }
@@ -1026,19 +1034,39 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   int w, s1;
   if (at < stop) prefetch_rows<F>(make_unit(&w, &s1), lane);
   if (!grid_barrier(p.sync + 1, &r, p)) return;
-  // h, 32 columns of a pair per warp: the parts of gate and of up joined
+  // h, 128 columns of a pair at a time: the parts of gate and of up joined, by a
+  // CTA where there is one for each task, else by a warp
   {
-    const int chunks = (p.f + 31) / 32;
-    for (int i = me; i < pairs * chunks; i += workers) {
-      const int q = i / chunks, j = i % chunks * 32 + lane;
-      const int unit = (j / 128 * G + r.group_of[q]) * 2;
-      const float* from = p.part1 + (size_t)q * 2 * p.f + j;
-      // MX4: f is a multiple of 32, every lane has a column
-      if (j < p.f) {
-        const int n = up.parts(unit), m = up.parts(unit + 1);
-        float g, v;
-        add_parts2(from, n, from + p.f, m, up_slab, &g, &v);
-        put_h<F>(p, q, j, g, v, lane);
+    const int tiles = (p.f + 127) / 128, tasks = pairs * tiles;
+    auto parts_of = [&](int q, int tile, int half, int i, int n) {  // the i-th of n shares of the parts
+      const int unit = (tile * G + r.group_of[q]) * 2 + half, parts = up.parts(unit);
+      return add_parts(p.part1 + ((size_t)q * 2 + half) * p.f + tile * 128 + 4 * lane, up_slab, parts * i / n,
+                       parts * (i + 1) / n);
+    };
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tasks <= (int)gridDim.x) {
+      const int q = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+      if (q < pairs) {
+        const bool in = tile * 128 + 4 * lane < p.f;
+        work.join[warp][lane] = in ? parts_of(q, tile, warp / 4, warp % 4, 4) : zero;
+        __syncthreads();
+        if (warp == 0) {
+          float4 s[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            s[half] = work.join[4 * half][lane];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) s[half] = add4(s[half], work.join[4 * half + i][lane]);
+          }
+          put_h<F>(p, q, tile * 128 + 4 * lane, s[0], s[1], in);
+        }
+      }
+    } else {
+      for (int i = me; i < tasks; i += workers) {
+        const int q = i / tiles, tile = i % tiles;
+        const bool in = tile * 128 + 4 * lane < p.f;
+        const float4 g = in ? parts_of(q, tile, 0, 0, 1) : zero, v = in ? parts_of(q, tile, 1, 0, 1) : zero;
+        put_h<F>(p, q, tile * 128 + 4 * lane, g, v, in);
       }
     }
   }
@@ -1059,31 +1087,32 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   if (!grid_barrier(p.sync + 3, &r, p)) return;
 
   // ------------------------------------------------------------------ y
-  // 32 columns of a token by `team` warps: warp i of the team joins the parts
-  // of the experts i, i + team, ...; their sums are added in the experts' order
+  // 128 columns of a token by a CTA: `per` warps join the parts of an expert;
+  // the experts' sums are added in their order
   {
-    const int team = p.k >= 8 ? 8 : p.k >= 4 ? 4 : p.k >= 2 ? 2 : 1;
-    const int chunks = (p.d + 31) / 32, tasks = p.M * chunks;
-    const int i_team = warp % team, per_cta = kWarps / team;
-    for (int base = blockIdx.x * per_cta; base < tasks; base += gridDim.x * per_cta) {
-      const int task = base + warp / team;
-      const int m = task / chunks, c = task % chunks * 32 + lane;
-      const bool in = task < tasks && c < p.d;
-      float y = 0.f;
-      for (int s0 = 0; s0 < p.k; s0 += team) {
-        const int s = s0 + i_team;
-        float v = 0.f;
-        if (in && s < p.k) {
-          const int q = m * p.k + s;
-          v = add_parts(p.part2 + (size_t)q * p.d + c, down_slab, down.parts(c / 128 * G + r.group_of[q]));
+    const int per = p.k > 4 ? 1 : p.k > 2 ? 2 : p.k == 2 ? 4 : 8, slots = kWarps / per;
+    const int tiles = (p.d + 127) / 128, tasks = p.M * tiles;
+    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+      const int m = task / tiles, tile = task % tiles, c = tile * 128 + 4 * lane;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s0 = 0; s0 < p.k; s0 += slots) {
+        const int s = s0 + warp / per;
+        if (s < p.k && c < p.d) {
+          const int q = m * p.k + s, parts = down.parts(tile * G + r.group_of[q]);
+          work.join[warp][lane] = add_parts(p.part2 + (size_t)q * p.d + c, down_slab, parts * (warp % per) / per,
+                                            parts * (warp % per + 1) / per);
         }
-        work.join[warp][lane] = v;
         __syncthreads();
-        if (i_team == 0 && in)
-          for (int i = 0; i < team && s0 + i < p.k; ++i) y = fmaf(r.gate[m * p.k + s0 + i], work.join[warp + i][lane], y);
+        if (warp == 0 && c < p.d)
+          for (int i = 0; i < slots && s0 + i < p.k; ++i) {
+            float4 v = work.join[i * per][lane];
+            for (int j = 1; j < per; ++j) v = add4(v, work.join[i * per + j][lane]);
+            const float gate = r.gate[m * p.k + s0 + i];
+            y = make_float4(fmaf(gate, v.x, y.x), fmaf(gate, v.y, y.y), fmaf(gate, v.z, y.z), fmaf(gate, v.w, y.w));
+          }
         __syncthreads();
       }
-      if (i_team == 0 && in) p.y[(size_t)m * p.d + c] = y;
+      if (warp == 0 && c < p.d) *reinterpret_cast<float4*>(p.y + (size_t)m * p.d + c) = y;
     }
   }
 
