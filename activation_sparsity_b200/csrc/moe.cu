@@ -92,6 +92,53 @@ struct MParams {
   unsigned long long wait_ns;
 };
 
+// How a phase's products are cut into shares for the warps: `units` (a group
+// and 128 columns) by `chunks` chunks of `rows` row steps (the last one may be
+// shorter).  Shares are taken in the order group, chunk, tile, so that the
+// warps at work read whole rows side by side.
+struct Cut {
+  int units, chunks, rows, shares;
+
+  // The most chunks: two or, with many rounds, kRounds shares per warp.
+  static __host__ __device__ int most(int units, int steps, int workers, int rounds) {
+    const int n = rounds * workers / units + 1;
+    return n < steps / kMinShare ? n : steps / kMinShare < 1 ? 1 : steps / kMinShare;
+  }
+  // Time of a phase in row steps: every round of shares costs its rows and a
+  // start, and the last share to end may lag by `lag` sixteenths of one.
+  static __device__ __forceinline__ int cost(int units, int steps, int workers, int c, int start, int lag) {
+    const int rows = (steps + c - 1) / c;
+    const int waves = (units * ((steps + rows - 1) / rows) + workers - 1) / workers;
+    return 16 * waves * (rows + start) + lag * rows;
+  }
+  // By a whole warp.
+  __device__ void choose(int units_, int steps, int workers, int rounds, int start, int lag) {
+    const int lane = threadIdx.x & 31;
+    const int n = most(units_, steps, workers, rounds);
+    unsigned best = 0xffffffffu, at = 1;
+    for (int c = lane + 1; c <= n; c += 32) {
+      const unsigned v = (unsigned)cost(units_, steps, workers, c, start, lag);
+      if (v < best) {
+        best = v;
+        at = c;
+      }
+    }
+    const unsigned least = __reduce_min_sync(0xffffffffu, best);
+    at = __reduce_min_sync(0xffffffffu, best == least ? at : 0xffffffffu);
+    if (lane == 0) {
+      units = units_;
+      rows = (steps + (int)at - 1) / (int)at;
+      chunks = (steps + rows - 1) / rows;
+      shares = units * chunks;
+    }
+  }
+  // A warp's first share: equally many neighbours for every CTA.
+  __device__ __forceinline__ int first(int warp) const {
+    const int per = min(kWarps, (shares + (int)gridDim.x - 1) / (int)gridDim.x);
+    return warp < per ? (int)blockIdx.x * per + warp : shares;
+  }
+};
+
 // The routing of a call, the same in every CTA.
 struct Routing {
   float gate[kMaxPairs];
@@ -99,7 +146,7 @@ struct Routing {
   short g_expert[kMaxPairs];
   short g_n[kMaxPairs];
   uint8_t g_pair[kMaxPairs][kGroup];
-  short group_of[kMaxPairs];
+  Cut up, down;  // gate | up, down
   int groups;
   int ok;
 };
@@ -416,7 +463,6 @@ __device__ void build_groups_warp(const MParams& p, Routing* r) {
   if (lane < pairs) {
     const int g = base + rank / kGroup;
     r->g_pair[g][rank % kGroup] = (uint8_t)lane;
-    r->group_of[lane] = (short)g;
     if (rank % kGroup == 0) {
       r->g_expert[g] = (short)e;
       r->g_n[g] = (short)min(kGroup, cnt - rank);
@@ -456,7 +502,6 @@ __device__ void build_groups(const MParams& p, Routing* r, Scratch* w) {
     for (int o = 0; o < q; ++o) rank += r->expert[o] == e;
     const int g = w->base[e] + rank / kGroup;
     r->g_pair[g][rank % kGroup] = (uint8_t)q;
-    r->group_of[q] = (short)g;
     if (rank % kGroup == 0) {
       r->g_expert[g] = (short)e;
       r->g_n[g] = (short)min(kGroup, w->cnt[e] - rank);
@@ -492,7 +537,9 @@ struct __align__(16) Stage {
 template <Fmt F>
 struct Cfg {
   static constexpr int kStep = F == Fmt::BF16 ? 16 : F == Fmt::F32 ? 8 : 32;  // rows of a step
-  static constexpr int kRounds = F == Fmt::MX4 ? 6 : 1;   // shares per warp
+  static constexpr int kRounds = F == Fmt::MX4 ? 8 : 2;   // shares per warp, at most
+  static constexpr int kStart = F == Fmt::MX4 ? 2 : 1;    // row steps that starting a share takes
+  static constexpr int kLag = F == Fmt::MX4 ? 12 : 4;     // sixteenths of a share
   static constexpr int kRing = 4;                         // MX4: stages of a warp's ring
   static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
                                       : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
@@ -849,38 +896,6 @@ __device__ __forceinline__ void put_h(const MParams& p, int q, int j, float4 g, 
   }
 }
 
-// The line of row steps of a phase: `units` units of `steps` each, cut into
-// `shares`.
-struct Line {
-  int steps;
-  long long total;
-  int shares;
-
-  // rounds: shares per warp, where they keep eight steps each.
-  __host__ __device__ Line(int units, int steps_, int workers, int rounds)
-      : steps(steps_), total((long long)units * steps_) {
-    const long long n = total / kMinShare, longer = total / 8;
-    if (n <= workers)
-      shares = n < 1 ? 1 : (int)n;
-    else
-      shares = longer <= workers ? workers : longer < (long long)rounds * workers ? (int)longer : rounds * workers;
-  }
-  // n / c; 32-bit division where the numbers allow it (a 64-bit one takes some
-  // hundred instructions).
-  static __device__ __forceinline__ long long div(long long n, long long c) {
-    return n >> 32 == 0 ? (long long)((unsigned)n / (unsigned)c) : n / c;
-  }
-  // First step of a share, and the share that holds a step.
-  __device__ __forceinline__ long long begin(int share) const { return div(total * share, shares); }
-  __device__ __forceinline__ int owner(long long at) const { return (int)div((at + 1) * shares - 1, total); }
-  __device__ __forceinline__ int unit(long long at) const { return (int)div(at, steps); }
-  // Shares that unit u's steps lie in: first, and how many.
-  __device__ __forceinline__ int first(int u) const { return owner((long long)u * steps); }
-  __device__ __forceinline__ int parts(int u) const { return owner((long long)(u + 1) * steps - 1) - first(u) + 1; }
-  // The most parts a unit can have.
-  int most_parts() const { return (int)((steps + total / shares - 1) / (total / shares)) + 1; }
-};
-
 // The next share of a warp beyond its first: asked for before the present one
 // is worked on (lane 0 holds the answer until then).
 __device__ __forceinline__ unsigned ask_share(unsigned* taken) {
@@ -978,68 +993,68 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
 
   // ------------------------------------------------------------------ gate | up
   // units: tile, group and half (gate, up), the last fastest
-  const Line up(G * 2 * ((p.f + 127) / 128), (p.d + kStep - 1) / kStep, workers, Cfg<F>::kRounds);
+  const int up_tiles = (p.f + 127) / 128, down_tiles = (p.d + 127) / 128;
+  if (warp == 0)
+    r.up.choose(G * 2 * up_tiles, (p.d + kStep - 1) / kStep, workers, Cfg<F>::kRounds, Cfg<F>::kStart, Cfg<F>::kLag);
+  else if (warp == 1)
+    r.down.choose(G * down_tiles, (p.f + kStep - 1) / kStep, workers, Cfg<F>::kRounds, Cfg<F>::kStart, Cfg<F>::kLag);
+  __syncthreads();
+  const Cut& up = r.up;
+  const Cut& down = r.down;
   const size_t up_slab = (size_t)pairs * 2 * p.f;
-  for (int share = me; share < up.shares;) {
+  const size_t up_bytes = row_bytes_of<F>(2 * p.f) * p.d;
+  // shares taken beyond the first of every warp are handed out in order
+  const int up_first = up.first(warp), up_taken = min(up.shares, kWarps * (int)gridDim.x);
+  for (int share = up_first; share < up.shares;) {
     const unsigned next = ask_share(p.sync + kTaken1);
-    const size_t expert_bytes = row_bytes_of<F>(2 * p.f) * p.d;
-    const long long stop = up.begin(share + 1);
-    for (long long at = up.begin(share); at < stop;) {
-      const int w = up.unit(at), s0 = (int)(at - (long long)w * up.steps);
-      const int s1 = (int)min((long long)up.steps, s0 + (stop - at));
-      const int group = w / 2 % G, tile = w / 2 / G, half = w % 2;
-      const int e = r.g_expert[group];
-      Unit u;
-      u.W = p.gu + (size_t)e * expert_bytes;
-      u.scales = F == Fmt::MX4 ? p.gus + (size_t)e * (p.d / 32) * (2 * p.f) : nullptr;
-      u.rows = p.d;
-      u.ld = 2 * p.f;
-      u.col = tile * 128 + half * p.f;
-      u.width = min(128, p.f - tile * 128);
-      u.n = r.g_n[group];
-      u.k0 = s0 * kStep;
-      u.k1 = min(p.d, s1 * kStep);
-      part_product<F, false>(p, &r, group, u, p.part1 + (size_t)(share - up.first(w)) * up_slab, 2 * p.f, smem);
-      at += s1 - s0;
-    }
-    share = workers + (int)__shfl_sync(0xffffffffu, next, 0);
+    const int column = share % (2 * up_tiles), rest = share / (2 * up_tiles);
+    const int chunk = rest % up.chunks, group = rest / up.chunks;
+    const int half = column >= up_tiles, tile = column - half * up_tiles;
+    const int e = r.g_expert[group];
+    Unit u;
+    u.W = p.gu + (size_t)e * up_bytes;
+    u.scales = F == Fmt::MX4 ? p.gus + (size_t)e * (p.d / 32) * (2 * p.f) : nullptr;
+    u.rows = p.d;
+    u.ld = 2 * p.f;
+    u.col = tile * 128 + half * p.f;
+    u.width = min(128, p.f - tile * 128);
+    u.n = r.g_n[group];
+    u.k0 = chunk * up.rows * kStep;
+    u.k1 = min(p.d, u.k0 + up.rows * kStep);
+    part_product<F, false>(p, &r, group, u, p.part1 + (size_t)chunk * up_slab, 2 * p.f, smem);
+    share = up_taken + (int)__shfl_sync(0xffffffffu, next, 0);
   }
 
   // ------------------------------------------------------------------ down
-  const Line down(G * ((p.d + 127) / 128), (p.f + kStep - 1) / kStep, workers, Cfg<F>::kRounds);
   const size_t down_slab = (size_t)pairs * p.d;
-  int share = me;
-  long long at = share < down.shares ? down.begin(share) : 0;
-  long long stop = share < down.shares ? down.begin(share + 1) : 0;
-  const size_t expert_bytes = row_bytes_of<F>(p.d) * p.f;
-  // this share's part of the unit at step `at`
-  auto make_unit = [&](int* w, int* s1) {
-    *w = down.unit(at);
-    const int s0 = (int)(at - (long long)*w * down.steps);
-    *s1 = (int)min((long long)down.steps, s0 + (stop - at));
-    const int group = *w % G, tile = *w / G;
-    const int e = r.g_expert[group];
+  const size_t down_bytes = row_bytes_of<F>(p.d) * p.f;
+  int share = down.first(warp);
+  const int down_taken = min(down.shares, kWarps * (int)gridDim.x);
+  auto make_unit = [&](int* group, int* chunk) {
+    const int tile = share % down_tiles, rest = share / down_tiles;
+    *chunk = rest % down.chunks;
+    *group = rest / down.chunks;
+    const int e = r.g_expert[*group];
     Unit u;
-    u.W = p.dn + (size_t)e * expert_bytes;
+    u.W = p.dn + (size_t)e * down_bytes;
     u.scales = F == Fmt::MX4 ? p.dns + (size_t)e * (p.f / 32) * p.d : nullptr;
     u.rows = p.f;
     u.ld = p.d;
     u.col = tile * 128;
     u.width = min(128, p.d - u.col);
-    u.n = r.g_n[group];
-    u.k0 = s0 * kStep;
-    u.k1 = min(p.f, *s1 * kStep);
+    u.n = r.g_n[*group];
+    u.k0 = *chunk * down.rows * kStep;
+    u.k1 = min(p.f, u.k0 + down.rows * kStep);
     return u;
   };
-  int w, s1;
-  if (at < stop) prefetch_rows<F>(make_unit(&w, &s1), lane);
+  int group, chunk;
+  if (share < down.shares) prefetch_rows<F>(make_unit(&group, &chunk), lane);
   if (!grid_barrier(p.sync + 1, &r, p)) return;
   // h, 128 columns of a pair at a time: the parts of gate and of up joined, by a
   // CTA where there is one for each task, else by a warp
   {
-    const int tiles = (p.f + 127) / 128, tasks = pairs * tiles;
+    const int tiles = up_tiles, tasks = pairs * tiles, parts = up.chunks;
     auto parts_of = [&](int q, int tile, int half, int i, int n) {  // the i-th of n shares of the parts
-      const int unit = (tile * G + r.group_of[q]) * 2 + half, parts = up.parts(unit);
       return add_parts(p.part1 + ((size_t)q * 2 + half) * p.f + tile * 128 + 4 * lane, up_slab, parts * i / n,
                        parts * (i + 1) / n);
     };
@@ -1073,16 +1088,9 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   if (!grid_barrier(p.sync + 2, &r, p)) return;
   while (share < down.shares) {
     const unsigned next = ask_share(p.sync + kTaken2);
-    while (at < stop) {
-      const Unit u = make_unit(&w, &s1);
-      part_product<F, true>(p, &r, w % G, u, p.part2 + (size_t)(share - down.first(w)) * down_slab, p.d, smem);
-      at = (long long)w * down.steps + s1;
-    }
-    share = workers + (int)__shfl_sync(0xffffffffu, next, 0);
-    if (share < down.shares) {
-      at = down.begin(share);
-      stop = down.begin(share + 1);
-    }
+    const Unit u = make_unit(&group, &chunk);
+    part_product<F, true>(p, &r, group, u, p.part2 + (size_t)chunk * down_slab, p.d, smem);
+    share = down_taken + (int)__shfl_sync(0xffffffffu, next, 0);
   }
   if (!grid_barrier(p.sync + 3, &r, p)) return;
 
@@ -1091,14 +1099,14 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   // the experts' sums are added in their order
   {
     const int per = p.k > 4 ? 1 : p.k > 2 ? 2 : p.k == 2 ? 4 : 8, slots = kWarps / per;
-    const int tiles = (p.d + 127) / 128, tasks = p.M * tiles;
+    const int tiles = down_tiles, tasks = p.M * tiles, parts = down.chunks;
     for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
       const int m = task / tiles, tile = task % tiles, c = tile * 128 + 4 * lane;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int s0 = 0; s0 < p.k; s0 += slots) {
         const int s = s0 + warp / per;
         if (s < p.k && c < p.d) {
-          const int q = m * p.k + s, parts = down.parts(tile * G + r.group_of[q]);
+          const int q = m * p.k + s;
           work.join[warp][lane] = add_parts(p.part2 + (size_t)q * p.d + c, down_slab, parts * (warp % per) / per,
                                             parts * (warp % per + 1) / per);
         }
@@ -1132,11 +1140,11 @@ MoePlan make_plan(int M, int d, int f, int E, int k, MoeFormat fmt) {
   const int rounds = fmt == MoeFormat::MX4 ? Cfg<Fmt::MX4>::kRounds : Cfg<Fmt::BF16>::kRounds;
   const int step = fmt == MoeFormat::BF16 ? 16 : fmt == MoeFormat::F32 ? 8 : 32;
   const int workers = 148 * kCtasPerSm * kWarps;
-  // A unit has the most parts where there are the fewest units: there are at
+  // A unit has the most chunks where there are the fewest units: there are at
   // least k groups (a token's experts differ) and one for every eight pairs.
   const int groups = std::max(k, (M * k + kGroup - 1) / kGroup);
-  const int parts1 = Line(groups * 2 * ((f + 127) / 128), (d + step - 1) / step, workers, rounds).most_parts();
-  const int parts2 = Line(groups * ((d + 127) / 128), (f + step - 1) / step, workers, rounds).most_parts();
+  const int parts1 = Cut::most(groups * 2 * ((f + 127) / 128), (d + step - 1) / step, workers, rounds);
+  const int parts2 = Cut::most(groups * ((d + 127) / 128), (f + step - 1) / step, workers, rounds);
   const size_t pairs = (size_t)M * k;
   size_t off = 0;
   auto take = [&](size_t bytes) {
