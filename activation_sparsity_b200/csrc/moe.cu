@@ -537,10 +537,10 @@ struct __align__(16) Stage {
 template <Fmt F>
 struct Cfg {
   static constexpr int kStep = F == Fmt::BF16 ? 16 : F == Fmt::F32 ? 8 : 32;  // rows of a step
-  static constexpr int kRounds = F == Fmt::MX4 ? 8 : 2;   // shares per warp, at most
+  static constexpr int kRounds = F == Fmt::MX4 ? 5 : 2;   // shares per warp, at most
   static constexpr int kStart = F == Fmt::MX4 ? 2 : 1;    // row steps that starting a share takes
   static constexpr int kLag = F == Fmt::MX4 ? 12 : 4;     // sixteenths of a share
-  static constexpr int kRing = 4;                         // MX4: stages of a warp's ring
+  static constexpr int kRing = 3;                         // MX4: stages of a warp's ring
   static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
                                       : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
                                                       : kRing * sizeof(Stage);
@@ -548,9 +548,10 @@ struct Cfg {
 };
 
 // Asynchronous copies to shared memory of `bytes` (all or none) bytes; the rest
-// is filled with zeros.
+// is filled with zeros.  By way of L1: the warps of a CTA mostly work on the
+// same rows, so that seven of eight find their operand there.
 __device__ __forceinline__ void copy16_or_zero(void* dst, const void* src, unsigned bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy4_or_zero(void* dst, const void* src, unsigned bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
