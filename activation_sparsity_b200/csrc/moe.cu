@@ -160,7 +160,10 @@ struct Scratch {
       int cnt[kMaxE];
       int base[kMaxE];
     };
-    unsigned long long key[kMaxE];  // selection by rank
+    struct {  // selection by rank: the scores' keys
+      unsigned hi[kMaxE];
+      unsigned lo[kMaxE];
+    };
   };
   int rank[kMaxE];
   double score[kMaxPairs];  // of the chosen experts
@@ -399,7 +402,9 @@ __device__ void route_by_rank(const MParams& p, Routing* r, Scratch* w) {
   bool bad = false;
   for (int i = tid; i < items; i += kT) {
     const double v = __ldcg(p.logits + i);
-    w->key[i] = score_key(v);
+    const unsigned long long key = score_key(v);
+    w->hi[i] = (unsigned)(key >> 32);
+    w->lo[i] = (unsigned)key;
     w->rank[i] = 0;
     bad |= !isfinite(v);
   }
@@ -409,11 +414,19 @@ __device__ void route_by_rank(const MParams& p, Routing* r, Scratch* w) {
   while (items * share * 2 <= kT) share *= 2;
   for (int i = tid; i < items * share; i += kT) {
     const int item = i / share, e = item % p.E;
-    const unsigned long long* row = w->key + item - e;
-    const unsigned long long mine = row[e];
+    const unsigned* row = w->hi + item - e;
+    const unsigned mine = row[e];
     const int from = i % share * p.E / share, to = (i % share + 1) * p.E / share;
-    int before = 0;
-    for (int o = from; o < to; ++o) before += row[o] > mine || (row[o] == mine && o < e);
+    int before = 0, same = 0;
+#pragma unroll 4
+    for (int o = from; o < to; ++o) {
+      before += row[o] > mine;
+      same += row[o] == mine;
+    }
+    if (same > (from <= e && e < to ? 1 : 0)) {  // others share the upper half
+      const unsigned* low = w->lo + item - e;
+      for (int o = from; o < to; ++o) before += row[o] == mine && (low[o] > low[e] || (low[o] == low[e] && o < e));
+    }
     if (share == 1)
       w->rank[item] = before;
     else
@@ -424,7 +437,7 @@ __device__ void route_by_rank(const MParams& p, Routing* r, Scratch* w) {
     const int rank = w->rank[i], m = i / p.E;
     if (rank < p.k) {
       r->expert[m * p.k + rank] = i % p.E;
-      w->score[m * p.k + rank] = key_score(w->key[i]);
+      w->score[m * p.k + rank] = key_score((unsigned long long)w->hi[i] << 32 | w->lo[i]);
     }
   }
   __syncthreads();
@@ -434,7 +447,7 @@ __device__ void route_by_rank(const MParams& p, Routing* r, Scratch* w) {
     float den = 0.f;
     if (!p.renormalize) {
       const double top = __shfl_sync(0xffffffffu, score, 0);
-      for (int e = lane; e < p.E; e += 32) den += expf((float)(key_score(w->key[m * p.E + e]) - top));
+      for (int e = lane; e < p.E; e += 32) den += expf((float)(key_score((unsigned long long)w->hi[m * p.E + e] << 32 | w->lo[m * p.E + e]) - top));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     }
@@ -971,7 +984,7 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   if (!grid_barrier(p.sync, &r, p)) return;
 
   // ------------------------------------------------------------------ routing
-  if (p.k >= 4 && p.E <= 128 && p.M * p.E <= kMaxE) {
+  if (p.k >= 4 && p.M * p.E <= kMaxE && p.M * p.E * p.E <= 4096 * p.k * ((p.M + kWarps - 1) / kWarps)) {
     route_by_rank(p, &r, &work);
   } else {
     for (int m = warp; m < p.M; m += kWarps) {
