@@ -146,15 +146,15 @@ __device__ __forceinline__ void add_parts(float* part, const RParams& p) {
 
 // Copies of a block's tile by one warp: `count` positions (a multiple of 8)
 // of 64 bytes, four lanes each, and the scales.  row(p) is the byte offset of
-// position p's row from `base`; lane chunks lie `chunk` bytes into a row.
+// position p's row from `base` (with the lane's chunk of the row).
 template <typename Row>
-__device__ __forceinline__ void copy_tile(mx4::Tile& tile, const uint8_t* base, uint32_t chunk, int count,
-                                          const uint8_t* scales, int lane, Row row) {
+__device__ __forceinline__ void copy_tile(mx4::Tile& tile, const uint8_t* base, int count, const uint8_t* scales,
+                                          int lane, Row row) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (8 * j < count) {
       const int pos = 8 * j + (lane >> 2);
-      mx4::copy16_l2(&tile.row[pos][16 * (lane & 3)], base + row(pos) + chunk);
+      mx4::copy16_l2(&tile.row[pos][16 * (lane & 3)], base + row(pos));
     }
   if (lane < 8) mx4::copy16_l2(&tile.scale[16 * lane], scales);
 }
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kRThreads, kFewCtas) mx4_rows_few_kernel(const
   // this lane's copies: 16 bytes of rows and of scales, the last ones where
   // they lie past the matrix
   const uint32_t chunk = min((uint32_t)col0 / 2 + 16u * (lane & 3), row_bytes - 16u);
-  const uint8_t* s_col = p.scales + min(col0 + 16 * lane, p.d_out - 16);
+  const uint32_t s_col = (uint32_t)min(col0 + 16 * lane, p.d_out - 16);
 
   float acc[1][8][2];
 #pragma unroll
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kRThreads, kFewCtas) mx4_rows_few_kernel(const
     pdl_launch_dependents();
     bool bad = false;
     const unsigned first = (unsigned)b_begin * 32u;
-    constexpr int kBatch = 8;  // entries in flight per thread
+    constexpr int kBatch = 16;  // entries in flight per thread
     for (int i0 = tid; i0 < p.K; i0 += kBatch * kRThreads) {
       unsigned r[kBatch];
       float v[kBatch];
@@ -297,28 +297,37 @@ __global__ void __launch_bounds__(kRThreads, kFewCtas) mx4_rows_few_kernel(const
     }
     __syncthreads();
 
-    auto copy = [&](int b, int stage_no) {
-      if (b < nb) {
-        const Packed<kM>& o = ops[b];
+    int b = warp / kHalves;
+    int at = b;  // the block the copies have come to, its rows and its scales
+    uint32_t rows_at = (uint32_t)(c0 + b) * 32u * row_bytes + chunk;  // a weight has at most 2^29 bytes
+    uint32_t scales_at = (uint32_t)(c0 + b) * (uint32_t)p.d_out + s_col;
+    auto copy = [&](mx4::Tile& tile) {
+      if (at < nb) {
+        const Packed<kM>& o = ops[at];
         const int n = o.n;
         if (n > 0)
-          copy_tile(ring[stage_no], p.codes + (size_t)(c0 + b) * 32 * row_bytes, chunk, (n + 7) & ~7,
-                    s_col + (size_t)(c0 + b) * p.d_out, lane, [&](int pos) { return o.off[pos]; });
+          copy_tile(tile, p.codes, (n + 7) & ~7, p.scales + scales_at, lane,
+                    [&](int pos) { return rows_at + o.off[pos]; });
       }
+      at += kLanes;
+      rows_at += kLanes * 32u * row_bytes;
+      scales_at += kLanes * (uint32_t)p.d_out;
       mx4::copies_commit();
     };
-    int b = warp / kHalves;
 #pragma unroll
-    for (int s = 0; s < kFewRing - 1; ++s) copy(b + s * kLanes, s);
-    for (int it = 0; b < nb; b += kLanes, ++it) {
+    for (int s = 0; s < kFewRing - 1; ++s) copy(ring[s]);
+    int now = 0, fill = kFewRing - 1;
+    for (; b < nb; b += kLanes) {
       __syncwarp();  // every lane has read the tile that is filled next
-      copy(b + (kFewRing - 1) * kLanes, (it + kFewRing - 1) % kFewRing);
+      copy(ring[fill]);
+      fill = fill + 1 == kFewRing ? 0 : fill + 1;
       mx4::copies_wait<kFewRing - 1>();
       __syncwarp();  // the other lanes' copies too
+      const mx4::Tile& tile = ring[now];
+      now = now + 1 == kFewRing ? 0 : now + 1;
       const Packed<kM>& o = ops[b];
       const int n = o.n;
       if (n == 0) continue;
-      const mx4::Tile& tile = ring[it % kFewRing];
       const float sx[1] = {o.sx[kM == 1 ? 0 : t]};
       mx4::RowSet rs;
       uint2 bop[2][1];
