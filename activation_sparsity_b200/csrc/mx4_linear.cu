@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
         const uint32_t ta = tmem + C::kD + s * C::kSfCols, tb = ta + 8;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          mx4::copy_scales<1>(ta + 4 * c, sfa + 512 * c);
-          mx4::copy_scales<1>(tb + 4 * c, sfb + 512 * c);
+          mx4::copy_scales(ta + 4 * c, sfa + 512 * c);
+          mx4::copy_scales(tb + 4 * c, sfb + 512 * c);
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)  // 64 inputs (32 bytes) each
@@ -228,11 +228,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
   if (!finished) *abort_flag = 1;
   __syncthreads();
   if (*abort_flag && warp == 4 && lane == 0) {
-    // let every copy this CTA armed land before its shared memory goes away;
-    // a stage whose scales never came cannot complete, so the wait is on the
-    // transfer alone where the limit ends it
+    // let the MMAs and every copy this CTA armed end before its memory goes
+    // away; a stage whose scales never came cannot complete and takes the whole
+    // time
+    mbar_wait_bounded(&done, 0, nullptr, mx4::kSettleNs);
     for (int it = max(0, issued - C::kStages); it < issued; ++it)
-      mbar_wait_bounded(&full[it % C::kStages], (it / C::kStages) & 1, nullptr, p.wait_ns);
+      mbar_wait_bounded(&full[it % C::kStages], (it / C::kStages) & 1, nullptr, mx4::kSettleNs);
     report(p.dev_status, LAROSA_DEV_TIMEOUT);
   }
   __syncthreads();

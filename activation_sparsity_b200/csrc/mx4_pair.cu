@@ -383,6 +383,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   // no CTA leaves while the other may still arrive at its barriers or read
   // its shared memory
   cluster.sync();
+  if (*abort_flag || *cluster.map_shared_rank(&s_abort, 1 - rank)) {
+    // what was issued for the pair ends before its memory goes away; a stage
+    // that was given up has no barrier that would tell
+    const unsigned long long t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < mx4::kSettleNs) {
+    }
+    __syncthreads();
+  }
   if (warp == 13) {
     tc::tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kRThreads, kFewCtas) mx4_rows_few_kernel(const
 
     int b = warp / kHalves;
     int at = b;  // the block the copies have come to, its rows and its scales
-    uint32_t rows_at = (uint32_t)(c0 + b) * 32u * row_bytes + chunk;  // a weight has at most 2^29 bytes
+    uint32_t rows_at = (uint32_t)(c0 + b) * 32u * row_bytes + chunk;  // a weight has at most 2^30 bytes
     uint32_t scales_at = (uint32_t)(c0 + b) * (uint32_t)p.d_out + s_col;
     auto copy = [&](mx4::Tile& tile) {
       if (at < nb) {

@@ -11,6 +11,11 @@ namespace mx4 {
 constexpr int kStageK = 256;  // inputs per pipeline stage: 128-byte rows of codes, the swizzle width
 constexpr int kStageBlocks = kStageK / kBlock;
 
+// How long a kernel that gives up lets the copies and MMAs it has issued end
+// before it frees what they use, whatever the wait limit: they take
+// microseconds, and the limit may be as short as one.
+constexpr unsigned long long kSettleNs = 100000;
+
 // Instruction descriptor of kind::mxf4: A and B e2m1 (1), K-major, scales
 // ue8m0, M = m, N = n; sf selects which half of a scale word the 64 inputs
 // take (0: bytes 0-1, 2: bytes 2-3).
@@ -33,12 +38,11 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, ui
 }
 
 // 512 bytes of scales (32 rows of 16 bytes) to four TMEM columns, in every
-// warp's lanes; with two CTAs, each from its own shared memory to its own TMEM.  Descriptor: no swizzle, groups of eight rows 128 bytes apart.
-template <int kGroup>
+// warp's lanes.  Descriptor: no swizzle, groups of eight rows 128 bytes apart.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr) {
   const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) |
                         ((uint64_t)1 << 46);
-  asm volatile("tcgen05.cp.cta_group::%2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc), "n"(kGroup) : "memory");
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
 // Eight scale bytes of a row from block kb on; zeros past the row's end.
