@@ -27,7 +27,8 @@
 //                              row-streaming GEMVs), y += y_r
 //   4-bit format               quantise / dequantise (mx4.cu); product of two
 //                              4-bit matrices mx4_linear_kernel (mx4_linear.cu,
-//                              tcgen05); sparse linear with a 4-bit weight:
+//                              tcgen05; from 65 tokens the scales' order and
+//                              mx4_pair_kernel, mx4_pair.cu); sparse linear with a 4-bit weight:
 //                              coefficients (topk.cu or mx4_coef_kernel, one
 //                              token's list by the product itself), then the
 //                              row kernels of mx4_rows.cu

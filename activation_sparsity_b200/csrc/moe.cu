@@ -23,17 +23,19 @@
 //            differ by less than fp32 rounding must not swap.  (Products of
 //            two fp32 values are exact in fp64.)
 //   routing  every CTA makes the same selection and the same work list from
-//            the scores.  A group is an expert and up to eight of its tokens;
-//            a unit is a group and 128 columns.
-//   products the row steps of all units, in order, are one line that is cut
-//            into equal shares for the warps of the grid: how many units there
-//            are is known only after the routing (5 tokens of 60 experts made
-//            396 units for 296 CTAs), and a share is one long stream of rows
-//            with no barrier in it.  A warp writes the sums of its part of a
-//            unit to the workspace;
-//   joins    after a barrier, the parts of every sum are added in the order of
-//            the line: h from gate and up, then y from the experts.  Results
-//            repeat bit for bit.
+//            the scores.  A group is an expert and up to eight of its tokens.
+//   products a unit is a group and 128 columns, cut into chunks of rows; a warp
+//            takes a unit's chunk as one stream with no barrier in it and
+//            writes its sums to the workspace.  How many units there are is
+//            known only after the routing, so every CTA chooses the same number
+//            of chunks there, the one that ends the last warp first.  Shares lie in
+//            the order group, chunk, tile: a CTA's eight warps read the same
+//            rows, side by side, and so do the CTAs at work.  With each warp on
+//            rows of its own the same bytes took a tenth longer (43 and 38.5 us
+//            for 128 bf16 experts of 2048 to 768, 262 and 234 for the 4-bit
+//            layer below).
+//   joins    after a barrier, the chunks' sums are added in their order: h from
+//            gate and up, then y from the experts.  Results repeat bit for bit.
 //
 // The products run on mma.sync.m16n8k16 with fp32 accumulators: eight tokens
 // of fp32 FMAs per 2-byte weight would be the limit instead of HBM.  A lane
@@ -43,7 +45,18 @@
 // of B.  The bf16 input is its own operand; h, an fp32 value, enters as three
 // bf16 pieces (24 significant bits) into the same accumulator.  4-bit experts
 // use the block products of mx4_mma.cuh, with x and h as two f16 pieces per
-// block of 32.  fp32 experts use fp32 FMAs.
+// block of 32 that travel through the warp's ring with the rows (loaded
+// straight from L2 they held up the stream: 299 and 266 us).  fp32 experts use
+// fp32 FMAs.
+//
+// Measured (B200, graph replay, weights from HBM): one token, 8 of 128 bf16
+// experts of 2048 to 768, 38.5 us (75 MB, 2.0 TB/s: 14 us outside the two
+// streams, which run at 4.0 TB/s); five tokens, 4 of 60 fp32 experts of 1024 to
+// 1408, 80 to 87 us (303 MB, 3.6 TB/s, from one placement of the weights to
+// another); 16 tokens, 2 of 8 4-bit experts of 4096 to 14336, 235 us (742 MB,
+// 3.2 TB/s: bound by issue and mma.sync, the same copies without the products
+// take 176 us); a layer of 8 bf16 experts of 256 to 512, 17.2 us, all of it the
+// chain of barriers.
 #include <algorithm>
 
 #include "common.cuh"
@@ -99,7 +112,8 @@ struct MParams {
 struct Cut {
   int units, chunks, rows, shares;
 
-  // The most chunks: two or, with many rounds, kRounds shares per warp.
+  // The most chunks that are considered: `rounds` shares per warp, of at least
+  // kMinShare steps.
   static __host__ __device__ int most(int units, int steps, int workers, int rounds) {
     const int n = rounds * workers / units + 1;
     return n < steps / kMinShare ? n : steps / kMinShare < 1 ? 1 : steps / kMinShare;
@@ -393,9 +407,7 @@ __device__ void route_token(const MParams& p, Routing* r, int m) {
 // Selection by the CTA for few scores in all (at most kMaxE): an expert's rank
 // is the number of its token's experts that come before it.  One pass of
 // comparisons spread over all threads, where a warp's k rounds of searching
-// for the largest take about 500 clocks each (a layer of 128 experts of 2048
-// to 768, one token, k = 8: 43.9 us with the rounds, 43.3 so; 8 experts of 256
-// to 512, k = 2: 18.0 and 19.1).
+// for the largest take about 500 clocks each.
 __device__ void route_by_rank(const MParams& p, Routing* r, Scratch* w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = p.M * p.E;
@@ -550,9 +562,15 @@ struct __align__(16) Stage {
 template <Fmt F>
 struct Cfg {
   static constexpr int kStep = F == Fmt::BF16 ? 16 : F == Fmt::F32 ? 8 : 32;  // rows of a step
-  static constexpr int kRounds = F == Fmt::MX4 ? 5 : 2;   // shares per warp, at most
-  static constexpr int kStart = F == Fmt::MX4 ? 2 : 1;    // row steps that starting a share takes
-  static constexpr int kLag = F == Fmt::MX4 ? 12 : 4;     // sixteenths of a share
+  // For Cut: shares per warp at most, row steps that starting a share takes, and
+  // sixteenths of a share that the last may lag.  4-bit shares take longer with
+  // more tokens, so several to a warp even them out (16 tokens of 8 experts of
+  // 4096 to 14336: at most three 247 us, five 234, eight 244); bf16 and fp32
+  // shares wait for HBM, and every further start costs more than it evens out
+  // (one token, 128 experts of 2048 to 768: up to two 38.5 us, up to four 44).
+  static constexpr int kRounds = F == Fmt::MX4 ? 5 : 2;
+  static constexpr int kStart = F == Fmt::MX4 ? 2 : 1;
+  static constexpr int kLag = F == Fmt::MX4 ? 12 : 4;
   static constexpr int kRing = 3;                         // MX4: stages of a warp's ring
   static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
                                       : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
@@ -984,6 +1002,9 @@ __global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
   if (!grid_barrier(p.sync, &r, p)) return;
 
   // ------------------------------------------------------------------ routing
+  // Ranks cost M E^2 comparisons over the CTA, rounds k searches for each of the
+  // tokens a warp has; one token of 128 experts, k = 8, gains 0.6 us by ranks,
+  // five tokens of 60, k = 4, and one of 8, k = 2, lose 2.5 and 0.5.
   if (p.k >= 4 && p.M * p.E <= kMaxE && p.M * p.E * p.E <= 4096 * p.k * ((p.M + kWarps - 1) / kWarps)) {
     route_by_rank(p, &r, &work);
   } else {

@@ -31,6 +31,10 @@
 // This kernel takes up to 64 tokens per tile; from there on pairs of SMs
 // share a tile (mx4_pair.cu).  Tokens vary fastest over the grid, so the CTAs
 // at work share weight tiles.
+//
+// Measured (B200, graph replay, from HBM): 3 tokens of 11008 x 4096, 12.1 us
+// (24 MB, 2.0 TB/s): about half is the way in and out, the launch, TMEM, the
+// first stage's latency and the splits' sum.
 #include <cooperative_groups.h>
 #include <cuda.h>
 

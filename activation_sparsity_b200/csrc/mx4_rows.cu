@@ -30,32 +30,41 @@
 //
 // A warp takes a block of 32 rows by 128 columns (64-byte row segments).  Its
 // rows arrive by asynchronous 16-byte copies in the warp's own ring of shared
-// memory tiles, two blocks ahead: a block is about 250 instructions, less
-// than the latency of its rows, and registers for more than one block in
+// memory tiles, two or three blocks ahead: registers for more than one block in
 // flight would halve the warps an SM holds.  Every copy is unconditional: an
 // empty slot names a row of the block that is read anyway (its coefficient is
 // zero), and columns past the matrix name the last ones (their sums are not
-// written).  A CTA's eight warps take the blocks of one split in turn and add
-// their sums in warp order through shared memory.  The splits of a column
-// tile write their sums to the workspace, and the last one to arrive adds
-// them in split order, so the result does not depend on timing.  (As
-// thread-block clusters with distributed shared memory the splits left SMs
-// empty: of clusters of seven, one CTA per SM, 15 fit the GPU at a time.)
+// written).  A CTA's warps take the blocks of one split in turn and add their
+// sums in warp order through shared memory.  The splits of a column tile write
+// their sums to the workspace, and the last one to arrive adds them in split
+// order, so the result does not depend on timing.  (As thread-block clusters
+// with distributed shared memory the splits left SMs empty: of clusters of
+// seven, one CTA per SM, 15 fit the GPU at a time.)
 //
 // Two ways to the B operand, by the number of tokens:
 //   up to 4 tokens   the CTA makes the operands of its split's blocks in
 //                    shared memory from the tokens' fp32 coefficients (a kept
-//                    list it scatters itself, or dense rows in global memory)
+//                    list it scatters itself, or dense rows in global memory),
+//                    both pieces of four tokens in one MMA's eight columns,
 //                    and packs the rows some token keeps into steps of 16 and
 //                    8 rows: at 60 % kept a block takes 24 of 32 slots.  One
 //                    or two warps abreast (128 or 256 columns per CTA) share
 //                    them;
-//   5 to 16 tokens   the operand is made once, by a few CTAs per token, and
-//                    copied along with the rows: making it in every column
-//                    tile would cost as much as the product.  Nearly every
-//                    row is kept by some token, so rows are not packed; one
-//                    that no token keeps is replaced by one that is read
-//                    anyway.
+//   5 to 16 tokens   the operand is made once, by four CTAs per token or by the
+//                    Top-K, and copied along with the rows: making it in every
+//                    column tile would cost as much as the product (348 us
+//                    where this takes 31).  An MMA holds one piece of eight
+//                    tokens, so that a lane's neighbouring accumulators are two
+//                    tokens and are scaled as pairs.  Nearly every row is kept
+//                    by some token, so rows are not packed; one that no token
+//                    keeps is replaced by one that is read anyway.
+//
+// Measured (B200, graph replay, weights from HBM): 2458 kept rows of 4096 x
+// 22016, one token, 17.3 us for a given list (35 MB: 2.0 TB/s) and 22.4 with
+// the Top-K before it; 8295 of 13824 x 5120, 16 tokens, 31.3 us with the operand
+// kernel (39 MB: 1.2 TB/s).  One token is bound by the chain before the first block (scanning the list about 2.5 us, packing 1.5) and
+// then by issue, about 250 instructions a block; 16 tokens by the rate of
+// mma.sync, 128 of them a block at about 2.1 clocks and SM: 17 us.
 #include <algorithm>
 
 #include "common.cuh"

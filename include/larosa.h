@@ -460,7 +460,9 @@ size_t larosa_mx4_linear_workspace_bytes(int M, int d_in, int d_out);
  *   y[m][j] = sum_k val[m][k] * W[idx[m][k]][j],
  * W [d_in x d_out] held as W_codes and W_scales with axis 0 (for example
  * larosa_prepare_weights' W_rot quantised with axis 0).  Only blocks and rows
- * that some token keeps are read.  idx/val as for larosa_sparse_linear; fp32
+ * that some token keeps are read.  idx/val as for larosa_sparse_linear (each
+ * token's indices distinct, in any order; an index that a token names twice
+ * takes one of the two values, the debug checks report it); fp32
  * accumulation, with the coefficients exact to 2^-24 of themselves (2^-50 of
  * the largest of their token within the 32 rows of a block); finite
  * coefficients below 2^100 in magnitude.  An index outside [0, d_in) sets
@@ -509,8 +511,9 @@ int larosa_mx4_topk_linear(const float *x_rot, const void *W_codes,
  * token's outputs are then unspecified (the indices within [0, E)).
  * ws: at least larosa_moe_workspace_bytes(M, d, f, E, k) bytes, zero-filled
  * before its first use; it holds counters that are zero between calls, so
- * calls sharing a workspace must not overlap.  The grid waits for itself
- * twice, within the wait limit (LAROSA_DEV_TIMEOUT beyond it).
+ * calls sharing a workspace must not overlap.  A cooperative launch (every CTA
+ * resident at once) whose grid waits for itself four times, each within the
+ * wait limit (LAROSA_DEV_TIMEOUT beyond it).
  */
 int larosa_moe_layer(const void *x, const void *Wr, const void *W_gu,
                      const void *S_gu, const void *W_d, const void *S_d, int M,
