@@ -21,9 +21,10 @@
 //           segments of codes out, the column maxima joined by two shuffles
 //           across the four row lanes.
 //
-// Measured (B200, graph replay, from HBM): 4096 x 22016 bf16, axis 0, 88.7 us
-// (5.1 TB/s, the columns' 128-byte segments do not fill a DRAM page); 777 x 11008
-// fp32, axis 1, 18.9 us (4.1 TB/s); one row of 4096, 2.1 us.
+// Measured (B200, graph replay, from HBM, one direction after the other): 4096 x
+// 22016 bf16, axis 0, 88.7 us (456 MB: 5.1 TB/s, the columns' 128-byte segments
+// do not fill a DRAM page); 777 x 11008 fp32, axis 1, 18.9 us (78 MB: 4.1 TB/s);
+// one row of 4096, 2.1 us.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"

@@ -33,10 +33,10 @@
 //         of both arrive too;
 //   13    one thread of the first CTA: MMAs for the pair; tcgen05.commit
 //         returns a stage, or hands over a tile, in both CTAs.
-// Measured (B200, graph replay): 4096 tokens of 5120 x 27648, bf16 out, 289 us
-// (4.0 PFLOP/s); 1111 of 4096 x 12288, 43.9 us (2.5 PFLOP/s: four rounds of tiles,
-// the last nine tenths full, and 9 us of the scales' pass, ramp and last
-// epilogue).  Bound by the copies out of L2: 36 bytes a clock reach an SM when
+// Measured (B200, graph replay, the tokens' quantising included): 4096 tokens of
+// 5120 x 27648, bf16 out, 289 us (4.0 PFLOP/s); 1111 of 4096 x 12288, 43.9 us (2.5
+// PFLOP/s: four rounds of tiles, the last nine tenths full, and about 9 us of
+// quantising, the scales' pass, ramp and last epilogue).  Bound by the copies out of L2: 36 bytes a clock reach an SM when
 // all ask, 800 clocks for a stage whose MMAs take 440 (NT = 192).
 //
 // Every wait is bounded; a CTA that gives up reports and leaves its loops, and
