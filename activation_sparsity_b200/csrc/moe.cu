@@ -50,12 +50,12 @@
 // fp32 FMAs.
 //
 // Measured (B200, graph replay, weights from HBM): one token, 8 of 128 bf16
-// experts of 2048 to 768, 38.5 us (75 MB, 2.0 TB/s: 14 us outside the two
-// streams, which run at 4.0 TB/s); five tokens, 4 of 60 fp32 experts of 1024 to
+// experts of 2048 to 768, 35.1 us (75 MB, 2.2 TB/s: 14 us outside the two
+// streams, which run at 3.6 TB/s); five tokens, 4 of 60 fp32 experts of 1024 to
 // 1408, 80 to 87 us (303 MB, 3.6 TB/s, from one placement of the weights to
 // another); 16 tokens, 2 of 8 4-bit experts of 4096 to 14336, 235 us (742 MB,
 // 3.2 TB/s: bound by issue and mma.sync, the same copies without the products
-// take 176 us); a layer of 8 bf16 experts of 256 to 512, 17.2 us, all of it the
+// take 176 us); a layer of 8 bf16 experts of 256 to 512, 16.6 us, all of it the
 // chain of barriers.
 #include <algorithm>
 
@@ -73,7 +73,6 @@ constexpr int kMaxE = 512;     // LAROSA_MOE_MAX_E
 constexpr int kMaxK = 16;      // LAROSA_MOE_MAX_K
 constexpr int kMaxPairs = 16 * kMaxK;
 constexpr int kMinShare = 2;    // row steps of a share, at least
-constexpr int kCtasPerSm = 2;
 
 enum class Fmt { BF16, F32, MX4 };
 
@@ -567,10 +566,15 @@ struct Cfg {
   // more tokens, so several to a warp even them out (16 tokens of 8 experts of
   // 4096 to 14336: at most three 247 us, five 234, eight 244); bf16 and fp32
   // shares wait for HBM, and every further start costs more than it evens out
-  // (one token, 128 experts of 2048 to 768: up to two 38.5 us, up to four 44).
+  // (one token, 128 experts of 2048 to 768: up to two 35.1 us, up to three 38.8).
   static constexpr int kRounds = F == Fmt::MX4 ? 5 : 2;
   static constexpr int kStart = F == Fmt::MX4 ? 2 : 1;
   static constexpr int kLag = F == Fmt::MX4 ? 12 : 4;
+  // CTAs per SM.  With one, bf16 products have the registers for two steps of
+  // 4 KB in flight per warp while a third is multiplied, and the barriers half as
+  // many arrivals (one token, 128 experts: 38.6 us with two CTAs, 35.1 with one;
+  // fp32 80 and 82, 4-bit 235 and 245).
+  static constexpr int kCtas = F == Fmt::BF16 ? 1 : 2;
   static constexpr int kRing = 3;                         // MX4: stages of a warp's ring
   static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
                                       : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
@@ -641,19 +645,21 @@ __device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16*
         for (int c = 0; c < P; ++c) mma_bf16(acc[seg][q], a0, a1, a2, a3, s.b[c]);
       }
   };
-  // two steps in turn, each loaded while the other is multiplied
-  Rows s0, s1;
+  // three steps in turn, two of them on their way while one is multiplied
+  Rows s0, s1, s2;
   int r = u.k0;
   load(r, s0);
+  if (r + 16 < u.k1) load(r + 16, s1);
   while (true) {
-    if (r + 16 < u.k1) load(r + 16, s1);
+    if (r + 32 < u.k1) load(r + 32, s2);
     multiply(s0);
-    r += 16;
-    if (r >= u.k1) break;
-    if (r + 16 < u.k1) load(r + 16, s0);
+    if ((r += 16) >= u.k1) break;
+    if (r + 32 < u.k1) load(r + 32, s0);
     multiply(s1);
-    r += 16;
-    if (r >= u.k1) break;
+    if ((r += 16) >= u.k1) break;
+    if (r + 32 < u.k1) load(r + 32, s1);
+    multiply(s2);
+    if ((r += 16) >= u.k1) break;
   }
 #pragma unroll
   for (int seg = 0; seg < 2; ++seg) {
@@ -970,7 +976,7 @@ __device__ __forceinline__ void prefetch_rows(const Unit& u, int lane) {
 }
 
 template <Fmt F>
-__global__ void __launch_bounds__(kT, kCtasPerSm) moe_kernel(const MParams p) {
+__global__ void __launch_bounds__(kT, Cfg<F>::kCtas) moe_kernel(const MParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Routing r;
   constexpr int kStep = Cfg<F>::kStep;
@@ -1174,7 +1180,10 @@ MoePlan make_plan(int M, int d, int f, int E, int k, MoeFormat fmt) {
   MoePlan pl;
   const int rounds = fmt == MoeFormat::MX4 ? Cfg<Fmt::MX4>::kRounds : Cfg<Fmt::BF16>::kRounds;
   const int step = fmt == MoeFormat::BF16 ? 16 : fmt == MoeFormat::F32 ? 8 : 32;
-  const int workers = 148 * kCtasPerSm * kWarps;
+  const int ctas = fmt == MoeFormat::MX4   ? Cfg<Fmt::MX4>::kCtas
+                   : fmt == MoeFormat::F32 ? Cfg<Fmt::F32>::kCtas
+                                           : Cfg<Fmt::BF16>::kCtas;
+  const int workers = 148 * ctas * kWarps;
   // A unit has the most chunks where there are the fewest units: there are at
   // least k groups (a token's experts differ) and one for every eight pairs.
   const int groups = std::max(k, (M * k + kGroup - 1) / kGroup);
@@ -1214,7 +1223,7 @@ cudaError_t launch_fmt(const MParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (per < 1) return cudaErrorLaunchOutOfResources;
     // at most the grid that the workspace is laid out for
-    grids[dev] = std::min(std::min(per, kCtasPerSm) * sms, kCtasPerSm * 148);
+    grids[dev] = std::min(std::min(per, Cfg<F>::kCtas) * sms, Cfg<F>::kCtas * 148);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grids[dev], 1, 1);
