@@ -558,6 +558,12 @@ struct __align__(16) Stage {
   __device__ __forceinline__ __half* chunk(int m, int c) { return &op[m][0][0] + 8 * (c ^ (2 * (m & 3))); }
 };
 
+// fp32: eight rows by 128 columns and the operands of up to eight tokens for them.
+struct __align__(16) RowStage {
+  float row[8][128];
+  float op[kGroup][8];
+};
+
 template <Fmt F>
 struct Cfg {
   static constexpr int kStep = F == Fmt::BF16 ? 16 : F == Fmt::F32 ? 8 : 32;  // rows of a step
@@ -575,9 +581,9 @@ struct Cfg {
   // many arrivals (one token, 128 experts: 38.6 us with two CTAs, 35.1 with one;
   // fp32 80 and 82, 4-bit 235 and 245).
   static constexpr int kCtas = F == Fmt::BF16 ? 1 : 2;
-  static constexpr int kRing = 3;                         // MX4: stages of a warp's ring
+  static constexpr int kRing = 3;  // fp32, MX4: stages of a warp's ring
   static constexpr size_t kWarpSmem = F == Fmt::BF16  ? 0
-                                      : F == Fmt::F32 ? 32 * kGroup * 4  // 32 rows of coefficients
+                                      : F == Fmt::F32 ? kRing * sizeof(RowStage)
                                                       : kRing * sizeof(Stage);
   static constexpr size_t kSmem = std::max(kWarps * kWarpSmem, sizeof(Scratch));
 };
@@ -677,64 +683,76 @@ __device__ __forceinline__ void product_bf16(const Unit& u, const __nv_bfloat16*
   }
 }
 
-// fp32 weights: a lane holds four columns; 32 rows' coefficients of every token
-// lie in the warp's shared memory.
-// op[i], out[i]: coefficients and sums of token i.
-template <int N>
-__device__ __forceinline__ void product_f32(const Unit& u, const float* const (&op)[kGroup],
-                                            float* const (&out)[kGroup], float* coef) {
+// fp32 weights: eight rows at a time, with their operands, through the warp's
+// ring of stages; a lane holds four columns.  mine: operand of token lane / 2 of
+// the group, its first row's (null: no token); out(m): where the sums of token m
+// go (null: nowhere).  (Rows in registers, eight in flight and eight being
+// multiplied, and operands loaded every 32 rows: 264 us where this takes 223, 16
+// tokens on 7 of 17 experts of 768 to 5184.)
+template <int N, typename Out>
+__device__ __forceinline__ void product_f32(const Unit& u, const float* mine, Out out, RowStage* ring) {
+  constexpr int kRing = Cfg<Fmt::F32>::kRing;
   const int lane = threadIdx.x & 31;
   const bool in = 4 * lane < u.width;
-  const int col = u.col + 4 * lane;
-  const float* base = reinterpret_cast<const float*>(u.W) + col;
+  const int col = u.col + 4 * lane, half = lane & 1;
+  const float* at = reinterpret_cast<const float*>(u.W) + (size_t)u.k0 * u.ld + col;
+  const int steps = (u.k1 - u.k0) / 8;
+  const unsigned present = mine != nullptr;
+  mine = present ? mine + u.k0 + 4 * half : reinterpret_cast<const float*>(u.W);  // else copies of no bytes: zeros
+  auto fetch = [&](RowStage& st) {
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx4::copy16_l2(&st.row[i][4 * lane], at + (size_t)i * u.ld);
+    }
+    if (lane < 2 * N) copy16_or_zero(&st.op[lane >> 1][4 * half], mine, present * 16);
+    at += (size_t)8 * u.ld;
+    mine += present * 8;
+  };
   float acc[N][4] = {};
-  constexpr int kBatch = N == 8 ? 4 : 8;  // rows in flight, twice: more spill at eight tokens
-  struct Rows {
-    float4 w[kBatch];
-  };
-  const float* next = base + (size_t)u.k0 * u.ld;
-  int loaded = u.k0;
-  auto load = [&](Rows& s) {
+  __syncwarp();  // the part before has read its stages
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      s.w[i] = in && loaded + i < u.k1 ? __ldcs(reinterpret_cast<const float4*>(next + (size_t)i * u.ld))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    next += (size_t)kBatch * u.ld;
-    loaded += kBatch;
-  };
-  auto multiply = [&](const Rows& s, int i0) {
+  for (int s = 0; s < kRing - 1; ++s) {
+    if (s < steps) fetch(ring[s]);
+    mx4::copies_commit();
+  }
+  int now = 0, fill = kRing - 1;
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    __syncwarp();  // every lane has read the stage that is filled next
+    if (i + kRing - 1 < steps) fetch(ring[fill]);
+    mx4::copies_commit();
+    mx4::copies_wait<kRing - 1>();
+    __syncwarp();  // the other lanes' copies too
+    const RowStage& st = ring[now];
+    now = now + 1 == kRing ? 0 : now + 1;
+    fill = fill + 1 == kRing ? 0 : fill + 1;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int h = 0; h < 2; ++h) {
+      float4 w[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4*>(&st.row[4 * h + r][4 * lane]);
 #pragma unroll
       for (int m = 0; m < N; ++m) {
-        const float v = coef[(i0 + i) * kGroup + m];
-        acc[m][0] = fmaf(v, s.w[i].x, acc[m][0]);
-        acc[m][1] = fmaf(v, s.w[i].y, acc[m][1]);
-        acc[m][2] = fmaf(v, s.w[i].z, acc[m][2]);
-        acc[m][3] = fmaf(v, s.w[i].w, acc[m][3]);
+        const float4 c = *reinterpret_cast<const float4*>(&st.op[m][4 * h]);
+        const float v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[m][0] = fmaf(v[r], w[r].x, acc[m][0]);
+          acc[m][1] = fmaf(v[r], w[r].y, acc[m][1]);
+          acc[m][2] = fmaf(v[r], w[r].z, acc[m][2]);
+          acc[m][3] = fmaf(v[r], w[r].w, acc[m][3]);
+        }
       }
-  };
-  Rows s0, s1;
-  load(s0);
-  for (int r0 = u.k0; r0 < u.k1; r0 += 32) {
-    __syncwarp();
-#pragma unroll
-    for (int m = 0; m < N; ++m)  // [row][token]; zero past the part
-      coef[lane * kGroup + m] = op[m] != nullptr && r0 + lane < u.k1 ? op[m][r0 + lane] : 0.f;
-    __syncwarp();
-#pragma unroll
-    for (int i0 = 0; i0 < 32; i0 += 2 * kBatch) {
-      if (r0 + i0 >= u.k1) break;
-      load(s1);
-      multiply(s0, i0);
-      load(s0);
-      multiply(s1, i0 + kBatch);
     }
   }
+  mx4::copies_wait<0>();
+  if (!in) return;
 #pragma unroll
-  for (int m = 0; m < N; ++m)
-    if (in && out[m] != nullptr)
-      __stcg(reinterpret_cast<float4*>(out[m] + col), make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]));
+  for (int m = 0; m < N; ++m) {
+    float* const to = out(m);
+    if (to != nullptr)
+      __stcg(reinterpret_cast<float4*>(to + col), make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]));
+  }
 }
 
 // MX4 weights: blocks of 32 rows, with their operands, through the warp's ring
@@ -856,23 +874,17 @@ __device__ __forceinline__ void part_product(const MParams& p, const Routing* r,
       product_bf16<1>(u, o < 0 ? nullptr : static_cast<const __nv_bfloat16*>(p.x) + (size_t)o * rows, o0, o1);
   } else if constexpr (F == Fmt::F32) {
     const float* src = kDown ? reinterpret_cast<const float*>(p.hop) : static_cast<const float*>(p.x);
-    const float* op[kGroup];
-    float* to[kGroup];
-#pragma unroll
-    for (int m = 0; m < kGroup; ++m) {
-      const int o = operand(m);
-      op[m] = o < 0 ? nullptr : src + (size_t)o * rows;
-      to[m] = sums_of(m);
-    }
-    float* coef = reinterpret_cast<float*>(smem + warp * Cfg<F>::kWarpSmem);
+    const int o = lane < 2 * kGroup ? operand(lane >> 1) : -1;
+    const float* mine = o < 0 ? nullptr : src + (size_t)o * rows;
+    RowStage* ring = reinterpret_cast<RowStage*>(smem + warp * Cfg<F>::kWarpSmem);
     if (u.n <= 1)
-      product_f32<1>(u, op, to, coef);
+      product_f32<1>(u, mine, sums_of, ring);
     else if (u.n <= 2)
-      product_f32<2>(u, op, to, coef);
+      product_f32<2>(u, mine, sums_of, ring);
     else if (u.n <= 4)
-      product_f32<4>(u, op, to, coef);
+      product_f32<4>(u, mine, sums_of, ring);
     else
-      product_f32<8>(u, op, to, coef);
+      product_f32<8>(u, mine, sums_of, ring);
   } else {
     const unsigned char* src = kDown ? p.hop : p.xop;
     const __half* pieces = reinterpret_cast<const __half*>(src);
