@@ -568,60 +568,67 @@ def larosa_dense_linear(x: torch.Tensor, Wt: torch.Tensor, y: torch.Tensor | Non
 
 # The calls below are short next to what Python spends around them (a one-token
 # product takes 5 to 10 us on the device), so they pass plain integers to
-# ctypes, ask for the raw stream and enter a device context only where the
-# tensors' device is not the current one.
+# ctypes, compare device numbers instead of device objects, ask for the raw
+# stream and enter a device context only where the tensors' device is not the
+# current one.
 
-def _need_fast(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device) -> None:
-    """_need, and on the device of the call's other tensors."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.device == device
-            and t.is_contiguous()):
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _need_fast(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> None:
+    """_need, and on the device (number) of the call's other tensors."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous()):
         _need(t, name, dtype)
-        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on cuda:{dev}")
 
 
-def _out(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, device) -> torch.Tensor:
-    """An output: allocated when not given, else checked (type, device, size)."""
-    if t is None:
-        return torch.empty(*shape, dtype=dtype, device=device)  # a third faster than with one tuple
-    _need_fast(t, name, dtype, device)
+def _need_out(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, dev: int) -> None:
+    """A given output: type, device, size."""
+    _need_fast(t, name, dtype, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
 
 
-def _call(fn, where: str, device: torch.device, *args) -> None:
-    """fn(*args, stream) on the tensors' device, on its current stream."""
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+def _call(where: str, dev: int, fn, args: tuple) -> None:
+    """fn(*args, stream) on device `dev`, on its current stream."""
+    if _current_device() == dev:
+        status = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
     if status != LAROSA_OK:
         raise LarosaError(status, where)
 
 
-def _status_word(dev_status: torch.Tensor | None, device: torch.device) -> int:
+def _status_word(dev_status: torch.Tensor | None, dev: int) -> int:
     if dev_status is None:
-        st = _status_cache.get(device.index)
-        return (default_status(device) if st is None else st).data_ptr()
-    _need_fast(dev_status, "dev_status", torch.int32, device)
+        st = _status_cache.get(dev)
+        return (default_status(torch.device("cuda", dev)) if st is None else st).data_ptr()
+    _need_fast(dev_status, "dev_status", torch.int32, dev)
     return dev_status.data_ptr()
 
 
-def _ws_pair(ws, device: torch.device, *sizes) -> tuple[int, int]:
+def _ws_pair(ws, dev: int, sizes: tuple) -> tuple[int, int]:
     """(address, bytes) of a workspace for these sizes; ws: a Workspace, a
     tensor, or None for the current stream's own."""
     if ws is None:
-        ws = _ws_cache.get((device.index, torch._C._cuda_getCurrentRawStream(device.index)))
+        ws = _ws_cache.get((dev, _raw_stream(dev)))
         if ws is None:
-            ws = default_workspace(device)
+            ws = default_workspace(torch.device("cuda", dev))
     if isinstance(ws, Workspace):
-        buf = (ws.get if len(sizes) == 4 else ws.get_moe if len(sizes) == 5 else ws.get_mx4_linear)(*sizes)
+        buf = ws.buf
+        n = buf.numel()  # of bytes
+        need = ws._need.get(sizes)
+        if need is None or n < need:
+            buf = (ws.get if len(sizes) == 4 else ws.get_moe if len(sizes) == 5 else ws.get_mx4_linear)(*sizes)
+            n = buf.numel()
     else:
         buf = ws
-    if buf.device != device:
-        raise ValueError(f"the workspace is on {buf.device}, the other tensors are on {device}")
-    return buf.data_ptr(), buf.numel() * buf.element_size()
+        n = buf.numel() * buf.element_size()
+    if buf.get_device() != dev:
+        raise ValueError(f"the workspace is on {buf.device}, the other tensors are on cuda:{dev}")
+    return buf.data_ptr(), n
 
 
 def _mx4_shapes(shape: tuple, axis: int) -> tuple[tuple, tuple, int, int]:
@@ -652,45 +659,55 @@ def larosa_mx4_quantize(src: torch.Tensor, axis: int = 1, codes: torch.Tensor | 
     32 along a row, scales [..., rows, cols / 32]; axis 0: down a column, scales
     [..., rows / 32, cols].  See larosa_mx4_quantize in the header."""
     _need(src, "src")
-    dev = src.device
+    dev, device = src.get_device(), src.device
     cs, ss, rows, cols = _mx4_shapes(src.shape, axis)
-    codes = _out(codes, "codes", cs, torch.uint8, dev)
-    scales = _out(scales, "scales", ss, torch.uint8, dev)
-    _call(_lib.larosa_mx4_quantize, "larosa_mx4_quantize", dev, src.data_ptr(), rows, cols, axis,
-          _dtype_code(src), codes.data_ptr(), scales.data_ptr(), _status_word(dev_status, dev))
+    if codes is None:
+        codes = torch.empty(*cs, dtype=torch.uint8, device=device)  # a third faster than with one tuple
+    else:
+        _need_out(codes, "codes", cs, torch.uint8, dev)
+    if scales is None:
+        scales = torch.empty(*ss, dtype=torch.uint8, device=device)
+    else:
+        _need_out(scales, "scales", ss, torch.uint8, dev)
+    _call("larosa_mx4_quantize", dev, _lib.larosa_mx4_quantize,
+          (src.data_ptr(), rows, cols, axis, _dtype_code(src), codes.data_ptr(), scales.data_ptr(),
+           _status_word(dev_status, dev)))
     return codes, scales
 
 
-def _mx4_pair(codes: torch.Tensor, scales: torch.Tensor, axis: int, what: str) -> tuple[int, int]:
-    """Checks a (codes, scales) pair; returns its (rows, cols)."""
-    if (codes.dim() == 2 and scales.dim() == 2 and codes.is_cuda and codes.dtype is torch.uint8
-            and scales.dtype is torch.uint8 and codes.is_contiguous() and scales.is_contiguous()
-            and scales.device == codes.device):
-        rows, half = codes.shape
-        s_rows, s_cols = scales.shape
-        if axis == 1 and s_rows == rows and s_cols * 16 == half:
-            return rows, 2 * half
-        if axis == 0 and s_rows * 32 == rows and s_cols == 2 * half and s_cols % 32 == 0:
-            return rows, s_cols
+def _mx4_pair(codes: torch.Tensor, scales: torch.Tensor, axis: int, what: str) -> tuple[int, int, int]:
+    """Checks a (codes, scales) pair; returns its (rows, cols, device number)."""
+    dev = codes.get_device()
+    shape = codes.shape
+    if (dev >= 0 and len(shape) == 2 and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
+            and scales.get_device() == dev and codes.is_contiguous() and scales.is_contiguous()):
+        rows, half = shape
+        if axis == 1:
+            if scales.shape == (rows, half // 16) and half % 16 == 0:
+                return rows, 2 * half, dev
+        elif scales.shape == (rows // 32, 2 * half) and rows % 32 == 0 and half % 16 == 0:
+            return rows, 2 * half, dev
     # a stack of matrices, or something to refuse
     _need(codes, what + "codes", torch.uint8)
-    _need_fast(scales, what + "scales", torch.uint8, codes.device)
-    shape = codes.shape
+    _need_fast(scales, what + "scales", torch.uint8, dev)
     if len(shape) < 2:
         raise ValueError(f"{what}codes must be a matrix or a stack of matrices")
     _, ss, rows, cols = _mx4_shapes((*shape[:-1], 2 * shape[-1]), axis)
     if scales.shape != ss:
         raise ValueError(f"{what}scales must have shape {ss}, got {tuple(scales.shape)}")
-    return rows, cols
+    return rows, cols, dev
 
 
 def larosa_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, axis: int = 1,
                           dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values that codes and scales (larosa_mx4_quantize) stand for."""
-    rows, cols = _mx4_pair(codes, scales, axis, "")
-    out = _out(out, "out", (*codes.shape[:-1], cols), dtype if out is None else out.dtype, codes.device)
-    _call(_lib.larosa_mx4_dequantize, "larosa_mx4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(),
-          rows, cols, axis, _dtype_code(out), out.data_ptr())
+    rows, cols, dev = _mx4_pair(codes, scales, axis, "")
+    if out is None:
+        out = torch.empty(*codes.shape[:-1], cols, dtype=dtype, device=codes.device)
+    else:
+        _need_out(out, "out", (*codes.shape[:-1], cols), out.dtype, dev)
+    _call("larosa_mx4_dequantize", dev, _lib.larosa_mx4_dequantize,
+          (codes.data_ptr(), scales.data_ptr(), rows, cols, axis, _dtype_code(out), out.data_ptr()))
     return out
 
 
@@ -704,18 +721,20 @@ def larosa_mx4_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, Wt_codes: t
     """y = x . W of two 4-bit matrices, [M, d_out] in `dtype`: x [M, d_in] and the
     weight in torch.nn.Linear layout [d_out, d_in], both of larosa_mx4_quantize
     with axis 1."""
-    M, d_in = _mx4_pair(x_codes, x_scales, 1, "x_")
-    d_out, d_w = _mx4_pair(Wt_codes, Wt_scales, 1, "Wt_")
-    dev = Wt_codes.device
+    M, d_in, x_dev = _mx4_pair(x_codes, x_scales, 1, "x_")
+    d_out, d_w, dev = _mx4_pair(Wt_codes, Wt_scales, 1, "Wt_")
     if d_w != d_in or x_codes.dim() != 2 or Wt_codes.dim() != 2:
         raise ValueError("x_codes must be [M, d_in / 2], Wt_codes [d_out, d_in / 2]")
-    if x_codes.device != dev:
-        raise ValueError(f"x_codes is on {x_codes.device}, the other tensors are on {dev}")
-    y = _out(y, "y", (M, d_out), dtype if y is None else y.dtype, dev)
-    p, n = _ws_pair(ws, dev, M, d_in, d_out)
-    _call(_lib.larosa_mx4_linear, "larosa_mx4_linear", dev, x_codes.data_ptr(), x_scales.data_ptr(),
-          Wt_codes.data_ptr(), Wt_scales.data_ptr(), M, d_in, d_out, y.data_ptr(), p, n,
-          _status_word(dev_status, dev), _dtype_code(y))
+    if x_dev != dev:
+        raise ValueError(f"x_codes is on {x_codes.device}, the other tensors are on cuda:{dev}")
+    if y is None:
+        y = torch.empty(M, d_out, dtype=dtype, device=Wt_codes.device)
+    else:
+        _need_out(y, "y", (M, d_out), y.dtype, dev)
+    p, n = _ws_pair(ws, dev, (M, d_in, d_out))
+    _call("larosa_mx4_linear", dev, _lib.larosa_mx4_linear,
+          (x_codes.data_ptr(), x_scales.data_ptr(), Wt_codes.data_ptr(), Wt_scales.data_ptr(), M, d_in, d_out,
+           y.data_ptr(), p, n, _status_word(dev_status, dev), _dtype_code(y)))
     return y
 
 
@@ -724,18 +743,21 @@ def larosa_mx4_sparse_linear(idx: torch.Tensor, val: torch.Tensor, W_codes: torc
                              ) -> torch.Tensor:
     """y = sum_k val[:, k] * W[idx[:, k]], fp32 [M, d_out], with a 4-bit weight
     (W_codes, W_scales of larosa_mx4_quantize(W, axis=0))."""
-    d_in, d_out = _mx4_pair(W_codes, W_scales, 0, "W_")
-    dev = W_codes.device
+    d_in, d_out, dev = _mx4_pair(W_codes, W_scales, 0, "W_")
     _need_fast(idx, "idx", torch.int32, dev)
     _need_fast(val, "val", torch.float32, dev)
     idx, val = _as2d(idx), _as2d(val)
     if idx.shape != val.shape or W_codes.dim() != 2:
         raise ValueError("idx and val must have one shape [M, K], W_codes [d_in, d_out / 2]")
     M, K = idx.shape
-    y = _out(y, "y", (M, d_out), torch.float32, dev)
-    p, n = _ws_pair(ws, dev, M, d_in, d_out, K)
-    _call(_lib.larosa_mx4_sparse_linear, "larosa_mx4_sparse_linear", dev, idx.data_ptr(), val.data_ptr(), M, K,
-          W_codes.data_ptr(), W_scales.data_ptr(), d_in, d_out, y.data_ptr(), p, n, _status_word(dev_status, dev))
+    if y is None:
+        y = torch.empty(M, d_out, dtype=torch.float32, device=W_codes.device)
+    else:
+        _need_out(y, "y", (M, d_out), torch.float32, dev)
+    p, n = _ws_pair(ws, dev, (M, d_in, d_out, K))
+    _call("larosa_mx4_sparse_linear", dev, _lib.larosa_mx4_sparse_linear,
+          (idx.data_ptr(), val.data_ptr(), M, K, W_codes.data_ptr(), W_scales.data_ptr(), d_in, d_out, y.data_ptr(),
+           p, n, _status_word(dev_status, dev)))
     return y
 
 
@@ -744,17 +766,20 @@ def larosa_mx4_topk_linear(x_rot: torch.Tensor, W_codes: torch.Tensor, W_scales:
                            ) -> torch.Tensor:
     """larosa_topk_linear with a 4-bit weight (W_codes, W_scales of
     larosa_mx4_quantize(W, axis=0)); the kept list stays in the workspace."""
-    d_in, d_out = _mx4_pair(W_codes, W_scales, 0, "W_")
-    dev = W_codes.device
+    d_in, d_out, dev = _mx4_pair(W_codes, W_scales, 0, "W_")
     _need_fast(x_rot, "x_rot", torch.float32, dev)
     x_rot = _as2d(x_rot)
-    M = x_rot.shape[0]
-    if x_rot.shape[1] != d_in or W_codes.dim() != 2:
+    M, d_x = x_rot.shape
+    if d_x != d_in or W_codes.dim() != 2:
         raise ValueError("x_rot must be [M, d_in], W_codes [d_in, d_out / 2]")
-    y = _out(y, "y", (M, d_out), torch.float32, dev)
-    p, n = _ws_pair(ws, dev, M, d_in, d_out, K)
-    _call(_lib.larosa_mx4_topk_linear, "larosa_mx4_topk_linear", dev, x_rot.data_ptr(), W_codes.data_ptr(),
-          W_scales.data_ptr(), M, d_in, d_out, K, y.data_ptr(), p, n, _status_word(dev_status, dev))
+    if y is None:
+        y = torch.empty(M, d_out, dtype=torch.float32, device=W_codes.device)
+    else:
+        _need_out(y, "y", (M, d_out), torch.float32, dev)
+    p, n = _ws_pair(ws, dev, (M, d_in, d_out, K))
+    _call("larosa_mx4_topk_linear", dev, _lib.larosa_mx4_topk_linear,
+          (x_rot.data_ptr(), W_codes.data_ptr(), W_scales.data_ptr(), M, d_in, d_out, K, y.data_ptr(), p, n,
+           _status_word(dev_status, dev)))
     return y
 
 
@@ -774,37 +799,48 @@ def larosa_moe_layer(x: torch.Tensor, Wr: torch.Tensor, W_gu: torch.Tensor, W_d:
     [E, f, d] of x's type; or 4-bit experts, W_gu and W_d the codes and S_gu, S_d
     the scales of larosa_mx4_quantize(W, axis=0)."""
     _need(x, "x")
-    dev, dt = x.device, x.dtype
+    dev, device, dt = x.get_device(), x.device, x.dtype
     x = _as2d(x)
     M, d = x.shape
     code = _dtype_code(x)
     _need_fast(Wr, "Wr", dt, dev)
     if (S_gu is None) != (S_d is None):
         raise ValueError("S_gu and S_d go together")
-    if W_gu.dim() != 3 or W_d.dim() != 3 or Wr.dim() != 2:
+    gu, dn = W_gu.shape, W_d.shape
+    if len(gu) != 3 or len(dn) != 3:
         raise ValueError("Wr must be [E, d], W_gu [E, d, 2 f], W_d [E, f, d]")
-    E, f = W_d.shape[0], W_d.shape[1]
+    E, f = dn[0], dn[1]
     if S_gu is None:
         _need_fast(W_gu, "W_gu", dt, dev)
         _need_fast(W_d, "W_d", dt, dev)
-        ok = W_gu.shape == (E, d, 2 * f) and W_d.shape[2] == d
+        ok = gu == (E, d, 2 * f) and dn[2] == d
         sg = sd = 0
     else:
         for t, name in ((W_gu, "W_gu"), (W_d, "W_d"), (S_gu, "S_gu"), (S_d, "S_d")):
             _need_fast(t, name, torch.uint8, dev)
         b = LAROSA_MX4_BLOCK
-        ok = (W_gu.shape == (E, d, f) and 2 * W_d.shape[2] == d and S_gu.shape == (E, d // b, 2 * f)
+        ok = (gu == (E, d, f) and 2 * dn[2] == d and S_gu.shape == (E, d // b, 2 * f)
               and S_d.shape == (E, f // b, d))
         sg, sd = S_gu.data_ptr(), S_d.data_ptr()
     if not ok or Wr.shape != (E, d):
         raise ValueError("shapes of x, Wr, the experts and their scales do not agree")
-    y = _out(y, "y", (M, d), torch.float32, dev)
-    idx = _out(idx, "idx", (M, k), torch.int32, dev)
-    gate = _out(gate, "gate", (M, k), torch.float32, dev)
-    p, n = _ws_pair(ws, dev, M, d, f, E, k)
-    _call(_lib.larosa_moe_layer, "larosa_moe_layer", dev, x.data_ptr(), Wr.data_ptr(), W_gu.data_ptr(), sg,
-          W_d.data_ptr(), sd, M, d, f, E, k, 1 if renormalize else 0, y.data_ptr(), idx.data_ptr(), gate.data_ptr(),
-          p, n, _status_word(dev_status, dev), code)
+    p, n = _ws_pair(ws, dev, (M, d, f, E, k))
+    if y is None:
+        y = torch.empty(M, d, dtype=torch.float32, device=device)
+    else:
+        _need_out(y, "y", (M, d), torch.float32, dev)
+    if idx is None:
+        idx = torch.empty(M, k, dtype=torch.int32, device=device)
+    else:
+        _need_out(idx, "idx", (M, k), torch.int32, dev)
+    if gate is None:
+        gate = torch.empty(M, k, dtype=torch.float32, device=device)
+    else:
+        _need_out(gate, "gate", (M, k), torch.float32, dev)
+    _call("larosa_moe_layer", dev, _lib.larosa_moe_layer,
+          (x.data_ptr(), Wr.data_ptr(), W_gu.data_ptr(), sg, W_d.data_ptr(), sd, M, d, f, E, k,
+           1 if renormalize else 0, y.data_ptr(), idx.data_ptr(), gate.data_ptr(), p, n,
+           _status_word(dev_status, dev), code))
     return y, idx, gate
 
 
