@@ -236,41 +236,42 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// Tasks (expert, four tokens), one CTA each.
-template <typename T>
+// Tasks (expert, kTok tokens), one CTA each.  Every load of a step is issued
+// before the first product, tokens past the last one read the last one's: with
+// a test per token the loads came one after the other (5 tokens of 3616 fp32
+// inputs 6.6 us, so 3.2).
+template <typename T, int kTok>
 __device__ void scores(const MParams& p, Scratch* r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tg = (p.M + 3) / 4;
+  const int tg = (p.M + kTok - 1) / kTok;
   const T* x = static_cast<const T*>(p.x);
   const T* wr = static_cast<const T*>(p.wr);
   for (int task = blockIdx.x; task < p.E * tg; task += gridDim.x) {
-    const int e = task / tg, m0 = task % tg * 4;
+    const int e = task / tg, m0 = task % tg * kTok;
     const T* w = wr + (size_t)e * p.d;
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 2
+    const T* row[kTok];
+#pragma unroll
+    for (int m = 0; m < kTok; ++m) row[m] = x + (size_t)min(m0 + m, p.M - 1) * p.d;
+    double acc[kTok] = {};
+#pragma unroll 1
     for (int i = threadIdx.x * 8; i < p.d; i += kT * 8) {
-      float wv[8];
+      float wv[8], xv[kTok][8];
       load8<T>(w + i, wv);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (m0 + m < p.M) {
-          float xv[8];
-          load8<T>(x + (size_t)(m0 + m) * p.d + i, xv);
+      for (int m = 0; m < kTok; ++m) load8<T>(row[m] + i, xv[m]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[m] = fma((double)wv[j], (double)xv[j], acc[m]);
-        }
-      }
+      for (int m = 0; m < kTok; ++m)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[m] = fma((double)wv[j], (double)xv[m][j], acc[m]);
     }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      if (m0 + m < p.M) {
+    for (int m = 0; m < kTok; ++m) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
-        if (lane == 0) r->sums[warp][m] = acc[m];
-      }
+      for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
+      if (lane == 0) r->sums[warp][m] = acc[m];
     }
     __syncthreads();
-    if (threadIdx.x < 4 && m0 + (int)threadIdx.x < p.M) {
+    if (threadIdx.x < kTok && m0 + (int)threadIdx.x < p.M) {
       double v = r->sums[0][threadIdx.x];
 #pragma unroll
       for (int i = 1; i < kWarps; ++i) v += r->sums[i][threadIdx.x];
@@ -278,6 +279,13 @@ __device__ void scores(const MParams& p, Scratch* r) {
     }
     __syncthreads();
   }
+}
+template <typename T>
+__device__ __forceinline__ void scores(const MParams& p, Scratch* r) {
+  if (p.M == 1)
+    scores<T, 1>(p, r);
+  else
+    scores<T, 4>(p, r);
 }
 
 // v of row `lane` of block `b` of token (or pair) m as MX4 pieces: op holds
@@ -495,43 +503,54 @@ __device__ void build_groups_warp(const MParams& p, Routing* r) {
   if (lane == 31) r->groups = incl;
 }
 
-// The groups of more pairs, by the CTA: experts in ascending order.
+// The groups of more pairs, by one warp, 32 pairs at a time: experts in ascending
+// order.
 __device__ void build_groups(const MParams& p, Routing* r, Scratch* w) {
-  const int tid = threadIdx.x;
+  const int lane = threadIdx.x & 31;
   const int pairs = p.M * p.k;
-  for (int e = tid; e < p.E; e += kT) w->cnt[e] = 0;
-  __syncthreads();
-  for (int q = tid; q < pairs; q += kT) atomicAdd(&w->cnt[r->expert[q]], 1);
-  __syncthreads();
-  if (tid < 32) {
-    int before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + tid;
-      const int n = e < p.E ? (w->cnt[e] + kGroup - 1) / kGroup : 0;
-      int incl = n;
+  constexpr int kRuns = kMaxPairs / 32;
+  for (int e = lane; e < p.E; e += 32) w->cnt[e] = 0;
+  __syncwarp();
+  int rank[kRuns];  // of a pair among its expert's
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (tid >= o) incl += v;
+  for (int c = 0; c < kRuns; ++c) {
+    if (32 * c >= pairs) break;
+    const int q = 32 * c + lane, e = q < pairs ? r->expert[q] : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int before = e < 0 ? 0 : w->cnt[e], here = __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (e >= 0 && here == 0) w->cnt[e] = before + __popc(same);
+    __syncwarp();
+    rank[c] = before + here;
+  }
+  int groups = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    const int n = e < p.E ? (w->cnt[e] + kGroup - 1) / kGroup : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (e < p.E) w->base[e] = groups + incl - n;
+    groups += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) r->groups = groups;
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < kRuns; ++c) {
+    if (32 * c >= pairs) break;
+    const int q = 32 * c + lane;
+    if (q < pairs) {
+      const int e = r->expert[q], g = w->base[e] + rank[c] / kGroup;
+      r->g_pair[g][rank[c] % kGroup] = (uint8_t)q;
+      if (rank[c] % kGroup == 0) {
+        r->g_expert[g] = (short)e;
+        r->g_n[g] = (short)min(kGroup, w->cnt[e] - rank[c]);
       }
-      if (e < p.E) w->base[e] = before + incl - n;
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (tid == 0) r->groups = before;
-  }
-  __syncthreads();
-  for (int q = tid; q < pairs; q += kT) {
-    const int e = r->expert[q];
-    int rank = 0;
-    for (int o = 0; o < q; ++o) rank += r->expert[o] == e;
-    const int g = w->base[e] + rank / kGroup;
-    r->g_pair[g][rank % kGroup] = (uint8_t)q;
-    if (rank % kGroup == 0) {
-      r->g_expert[g] = (short)e;
-      r->g_n[g] = (short)min(kGroup, w->cnt[e] - rank);
     }
   }
-  __syncthreads();
 }
 
 // ---------------------------------------------------------------- products
@@ -1036,12 +1055,13 @@ __global__ void __launch_bounds__(kT, Cfg<F>::kCtas) moe_kernel(const MParams p)
     }
     __syncthreads();
   }
-  if (pairs <= 32) {
-    if (warp == 0) build_groups_warp(p, &r);
-    __syncthreads();
-  } else {
-    build_groups(p, &r, &work);
+  if (warp == 0) {
+    if (pairs <= 32)
+      build_groups_warp(p, &r);
+    else
+      build_groups(p, &r, &work);
   }
+  __syncthreads();
   const int G = r.groups;
 
   // ------------------------------------------------------------------ gate | up
