@@ -72,6 +72,7 @@ constexpr int kGroup = 8;      // tokens of a group
 constexpr int kMaxE = 512;     // LAROSA_MOE_MAX_E
 constexpr int kMaxK = 16;      // LAROSA_MOE_MAX_K
 constexpr int kMaxPairs = 16 * kMaxK;
+constexpr int kMaxRanked = 512;  // scores that are selected by rank
 constexpr int kMinShare = 2;    // row steps of a share, at least
 
 enum class Fmt { BF16, F32, MX4 };
@@ -118,19 +119,24 @@ struct Cut {
     return n < steps / kMinShare ? n : steps / kMinShare < 1 ? 1 : steps / kMinShare;
   }
   // Time of a phase in row steps: every round of shares costs its rows and a
-  // start, and the last share to end may lag by `lag` sixteenths of one.
-  static __device__ __forceinline__ int cost(int units, int steps, int workers, int c, int start, int lag) {
-    const int rows = (steps + c - 1) / c;
-    const int waves = (units * ((steps + rows - 1) / rows) + workers - 1) / workers;
-    return 16 * waves * (rows + start) + lag * rows;
+  // start, and the last share to end may lag by `lag` sixteenths of one.  In
+  // floating point, whose divisions take a tenth of the whole numbers' time: a
+  // quotient that is a whole number may come out a little larger, hence the
+  // offsets (fractions are at least 1 / 2368).
+  static __device__ __forceinline__ float cost(int units, int steps, int workers, int c, int start, int lag) {
+    const float rows = ceilf(__fdividef((float)steps, (float)c) - 2e-4f);
+    const float shares = (float)units * ceilf(__fdividef((float)steps, rows) - 2e-4f);
+    const float waves = ceilf(__fdividef(shares, (float)workers) - 2e-4f);
+    return 16.f * waves * (rows + (float)start) + (float)lag * rows;
   }
   // By a whole warp.
   __device__ void choose(int units_, int steps, int workers, int rounds, int start, int lag) {
     const int lane = threadIdx.x & 31;
     const int n = most(units_, steps, workers, rounds);
-    unsigned best = 0xffffffffu, at = 1;
+    unsigned best = 0xffffffffu, at = 1;  // costs are positive: their bits compare as they do
+#pragma unroll 1
     for (int c = lane + 1; c <= n; c += 32) {
-      const unsigned v = (unsigned)cost(units_, steps, workers, c, start, lag);
+      const unsigned v = __float_as_uint(cost(units_, steps, workers, c, start, lag));
       if (v < best) {
         best = v;
         at = c;
@@ -174,11 +180,11 @@ struct Scratch {
       int base[kMaxE];
     };
     struct {  // selection by rank: the scores' keys
-      unsigned hi[kMaxE];
-      unsigned lo[kMaxE];
+      unsigned hi[kMaxRanked];
+      unsigned lo[kMaxRanked];
     };
   };
-  int rank[kMaxE];
+  int rank[kMaxRanked];     // scores: in their token's order; pairs: among their expert's
   double score[kMaxPairs];  // of the chosen experts
   double sums[kWarps][4];   // scores: the warps' shares
   float4 join[kWarps][32];  // the warps' shares of a sum of parts
@@ -411,7 +417,7 @@ __device__ void route_token(const MParams& p, Routing* r, int m) {
   write_gates(p, r, m, expert, score, den);
 }
 
-// Selection by the CTA for few scores in all (at most kMaxE): an expert's rank
+// Selection by the CTA for few scores in all (at most kMaxRanked): an expert's rank
 // is the number of its token's experts that come before it.  One pass of
 // comparisons spread over all threads, where a warp's k rounds of searching
 // for the largest take about 500 clocks each.
@@ -504,31 +510,29 @@ __device__ void build_groups_warp(const MParams& p, Routing* r) {
 }
 
 // The groups of more pairs, by one warp, 32 pairs at a time: experts in ascending
-// order.
+// order.  (Loops are not unrolled here: code that runs once costs more to fetch
+// than to run, 3.2 us for 112 pairs with both loops unrolled.)
 __device__ void build_groups(const MParams& p, Routing* r, Scratch* w) {
   const int lane = threadIdx.x & 31;
   const int pairs = p.M * p.k;
-  constexpr int kRuns = kMaxPairs / 32;
   for (int e = lane; e < p.E; e += 32) w->cnt[e] = 0;
   __syncwarp();
-  int rank[kRuns];  // of a pair among its expert's
-#pragma unroll
-  for (int c = 0; c < kRuns; ++c) {
-    if (32 * c >= pairs) break;
-    const int q = 32 * c + lane, e = q < pairs ? r->expert[q] : -1;
+#pragma unroll 1
+  for (int q = lane; q < (pairs + 31) / 32 * 32; q += 32) {
+    const int e = q < pairs ? r->expert[q] : -1;
     const unsigned same = __match_any_sync(0xffffffffu, e);
     const int before = e < 0 ? 0 : w->cnt[e], here = __popc(same & ((1u << lane) - 1u));
     __syncwarp();
     if (e >= 0 && here == 0) w->cnt[e] = before + __popc(same);
     __syncwarp();
-    rank[c] = before + here;
+    w->rank[q] = before + here;
   }
   int groups = 0;
   for (int e0 = 0; e0 < p.E; e0 += 32) {
     const int e = e0 + lane;
     const int n = e < p.E ? (w->cnt[e] + kGroup - 1) / kGroup : 0;
     int incl = n;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
@@ -538,17 +542,13 @@ __device__ void build_groups(const MParams& p, Routing* r, Scratch* w) {
   }
   if (lane == 0) r->groups = groups;
   __syncwarp();
-#pragma unroll
-  for (int c = 0; c < kRuns; ++c) {
-    if (32 * c >= pairs) break;
-    const int q = 32 * c + lane;
-    if (q < pairs) {
-      const int e = r->expert[q], g = w->base[e] + rank[c] / kGroup;
-      r->g_pair[g][rank[c] % kGroup] = (uint8_t)q;
-      if (rank[c] % kGroup == 0) {
-        r->g_expert[g] = (short)e;
-        r->g_n[g] = (short)min(kGroup, w->cnt[e] - rank[c]);
-      }
+#pragma unroll 1
+  for (int q = lane; q < pairs; q += 32) {
+    const int e = r->expert[q], rank = w->rank[q], g = w->base[e] + rank / kGroup;
+    r->g_pair[g][rank % kGroup] = (uint8_t)q;
+    if (rank % kGroup == 0) {
+      r->g_expert[g] = (short)e;
+      r->g_n[g] = (short)min(kGroup, w->cnt[e] - rank);
     }
   }
 }
@@ -1040,9 +1040,10 @@ __global__ void __launch_bounds__(kT, Cfg<F>::kCtas) moe_kernel(const MParams p)
 
   // ------------------------------------------------------------------ routing
   // Ranks cost M E^2 comparisons over the CTA, rounds k searches for each of the
-  // tokens a warp has; one token of 128 experts, k = 8, gains 0.6 us by ranks,
-  // five tokens of 60, k = 4, and one of 8, k = 2, lose 2.5 and 0.5.
-  if (p.k >= 4 && p.M * p.E <= kMaxE && p.M * p.E * p.E <= 4096 * p.k * ((p.M + kWarps - 1) / kWarps)) {
+  // tokens a warp has.  One token of 128 experts, k = 8, gains 0.5 us by ranks and
+  // one of 75, k = 6, 0.4; one of 8, k = 2, loses 0.5, five of 60, k = 4, 2.5 and
+  // five of 143, k = 4, 5.
+  if (p.k >= 4 && p.M * p.E <= kMaxRanked && p.M * p.E * p.E <= 4096 * p.k * ((p.M + kWarps - 1) / kWarps)) {
     route_by_rank(p, &r, &work);
   } else {
     for (int m = warp; m < p.M; m += kWarps) {
@@ -1067,10 +1068,12 @@ __global__ void __launch_bounds__(kT, Cfg<F>::kCtas) moe_kernel(const MParams p)
   // ------------------------------------------------------------------ gate | up
   // units: tile, group and half (gate, up), the last fastest
   const int up_tiles = (p.f + 127) / 128, down_tiles = (p.d + 127) / 128;
-  if (warp == 0)
-    r.up.choose(G * 2 * up_tiles, (p.d + kStep - 1) / kStep, workers, Cfg<F>::kRounds, Cfg<F>::kStart, Cfg<F>::kLag);
-  else if (warp == 1)
-    r.down.choose(G * down_tiles, (p.f + kStep - 1) / kStep, workers, Cfg<F>::kRounds, Cfg<F>::kStart, Cfg<F>::kLag);
+  if (warp < 2) {
+    const bool first = warp == 0;
+    Cut& cut = first ? r.up : r.down;
+    cut.choose(G * (first ? 2 * up_tiles : down_tiles), ((first ? p.d : p.f) + kStep - 1) / kStep, workers,
+               Cfg<F>::kRounds, Cfg<F>::kStart, Cfg<F>::kLag);
+  }
   __syncthreads();
   const Cut& up = r.up;
   const Cut& down = r.down;
