@@ -47,16 +47,16 @@
 // use the block products of mx4_mma.cuh, with x and h as two f16 pieces per
 // block of 32 that travel through the warp's ring with the rows (loaded
 // straight from L2 they held up the stream: 299 and 266 us).  fp32 experts use
-// fp32 FMAs.
+// fp32 FMAs on rows that come through a ring as well.
 //
 // Measured (B200, graph replay, weights from HBM): one token, 8 of 128 bf16
-// experts of 2048 to 768, 35.1 us (75 MB, 2.2 TB/s: 14 us outside the two
+// experts of 2048 to 768, 34.5 us (75 MB, 2.2 TB/s: 13 us outside the two
 // streams, which run at 3.6 TB/s); five tokens, 4 of 60 fp32 experts of 1024 to
-// 1408, 80 to 87 us (303 MB, 3.6 TB/s, from one placement of the weights to
-// another); 16 tokens, 2 of 8 4-bit experts of 4096 to 14336, 235 us (742 MB,
+// 1408, 80 to 83 us (303 MB, 3.7 TB/s, from one placement of the weights to
+// another); 16 tokens, 2 of 8 4-bit experts of 4096 to 14336, 234 us (742 MB,
 // 3.2 TB/s: bound by issue and mma.sync, the same copies without the products
-// take 176 us); a layer of 8 bf16 experts of 256 to 512, 16.6 us, all of it the
-// chain of barriers.
+// take 176 us); a layer of 8 bf16 experts of 256 to 512, 15.6 us, all of it the
+// chain of barriers and the first fetch of each phase's code.
 #include <algorithm>
 
 #include "common.cuh"
