@@ -22,9 +22,8 @@
 //           across the four row lanes.
 //
 // Measured (B200, graph replay, from HBM, one direction after the other): 4096 x
-// 22016 bf16, axis 0, 88.7 us (456 MB: 5.1 TB/s, the columns' 128-byte segments
-// do not fill a DRAM page); 777 x 11008 fp32, axis 1, 18.9 us (78 MB: 4.1 TB/s);
-// one row of 4096, 2.1 us.
+// 22016 bf16, axis 0, 77.4 us (456 MB: 5.9 TB/s, the copy rate being 6.5); 777 x
+// 11008 fp32, axis 1, 13.5 us (78 MB: 5.7 TB/s); one row of 4096, 2.1 us.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"
@@ -76,8 +75,17 @@ struct Eight<float> {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
   static __device__ __forceinline__ void store(void* base, size_t i, const float (&v)[8]) {
-    reinterpret_cast<float4*>(base)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(base)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    // 32 bytes at once where the matrix is aligned so: two 16-byte stores of a
+    // warp leave every other half sector to each other (4.2 and 6.3 TB/s)
+    float* at = static_cast<float*>(base) + 8 * i;
+    if ((reinterpret_cast<uintptr_t>(base) & 31u) == 0) {
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "f"(v[0]), "f"(v[1]),
+                   "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<float4*>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
   }
 };
 
@@ -131,9 +139,44 @@ __global__ void __launch_bounds__(kQThreads)
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) report(dev_status, LAROSA_DEV_NONFINITE);
 }
 
+// The largest magnitudes of eight columns, as bits; those of bf16 in pairs, as
+// they are loaded: one by one the maxima cost a third of the time of a pass
+// over bf16 (axis 0: 51.6 and 40.2 us for 4096 x 22016).
+template <typename T>
+struct Tops;
+template <>
+struct Tops<__nv_bfloat16> {
+  uint32_t m[4] = {0u, 0u, 0u, 0u};
+  __device__ __forceinline__ void add(const Eight<__nv_bfloat16>& e) {
+    const uint32_t w[4] = {e.u.x, e.u.y, e.u.z, e.u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = __vmaxu2(m[k], w[k] & 0x7fff7fffu);
+  }
+  __device__ __forceinline__ void join(int lanes) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], lanes));
+  }
+  __device__ __forceinline__ uint32_t bits(int k) const { return k & 1 ? m[k / 2] & 0xffff0000u : m[k / 2] << 16; }
+};
+template <>
+struct Tops<float> {
+  uint32_t m[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  __device__ __forceinline__ void add(const Eight<float>& e) {
+    float v[8];
+    e.get(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m[k] = max(m[k], abs_bits(v[k]));
+  }
+  __device__ __forceinline__ void join(int lanes) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], lanes));
+  }
+  __device__ __forceinline__ uint32_t bits(int k) const { return m[k]; }
+};
+
 // Axis 0: warp tile 32 rows x 64 columns; cg = cols / 8 column groups.
 template <typename T>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 4 : 2)
     quantize_cols_kernel(const void* __restrict__ src, int row_blocks, int cg, uint32_t* __restrict__ codes,
                          uint8_t* __restrict__ scales, int* dev_status) {
   pdl_wait();
@@ -156,21 +199,16 @@ __global__ void __launch_bounds__(kQThreads)
       else
         e[i].zero();
     }
-    uint32_t m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    Tops<T> top;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v[8];
-      e[i].get(v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m[k] = max(m[k], abs_bits(v[k]));
-    }
+    for (int i = 0; i < 8; ++i) top.add(e[i]);
+    top.join(8);
+    top.join(16);
     float inv[8];
     uint32_t sb[2] = {0, 0}, ok = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], 8));
-      m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], 16));
-      const uint32_t b = mx4::scale_byte(m[k]);
+      const uint32_t b = mx4::scale_byte(top.bits(k));
       sb[k >> 2] |= b << (8 * (k & 3));
       bad |= b == 255u;
       ok |= (b == 255u ? 0u : 0xfu) << (4 * k);

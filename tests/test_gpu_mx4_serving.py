@@ -162,3 +162,20 @@ def test_a_wait_limit_too_short_for_the_product(L, M):
     again = L.larosa_mx4_linear(xc, xs, wc, ws, dev_status=st)
     assert L.larosa_check(st) == 0 and torch.equal(again, want)
     linear.check(f64(again), x, w, torch.float32)
+
+
+@pytest.mark.parametrize("axis", [0, 1])
+def test_values_go_to_any_16_byte_boundary(L, axis):
+    """Outputs that start 16, 32 and 48 bytes into an allocation; what lies
+    around them stays."""
+    x = sd.activations(64, 160, 270, torch.float32).cuda()
+    codes, scales = L.larosa_mx4_quantize(x, axis=axis)
+    want = L.larosa_mx4_dequantize(codes, scales, axis=axis)
+    for dtype, step in ((torch.float32, 4), (torch.bfloat16, 8)):
+        for k in (1, 2, 3):
+            buf = torch.full((64 * 160 + 64,), 7.0, dtype=dtype, device="cuda")
+            out = buf[k * step:k * step + 64 * 160].view(64, 160)
+            L.larosa_mx4_dequantize(codes, scales, axis=axis, out=out)
+            assert torch.equal(out, want.to(dtype))
+            rest = torch.cat([buf[:k * step], buf[k * step + 64 * 160:]])
+            assert torch.all(rest == 7.0)
