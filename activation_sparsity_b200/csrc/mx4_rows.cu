@@ -50,7 +50,7 @@
 //                    8 rows: at 60 % kept a block takes 24 of 32 slots.  One
 //                    or two warps abreast (128 or 256 columns per CTA) share
 //                    them;
-//   5 to 16 tokens   the operand is made once, by four CTAs per token or by the
+//   5 to 16 tokens   the operand is made once, by eight CTAs per token or by the
 //                    Top-K, and copied along with the rows: making it in every
 //                    column tile would cost as much as the product (348 us
 //                    where this takes 31).  An MMA holds one piece of eight
@@ -61,7 +61,7 @@
 //
 // Measured (B200, graph replay, weights from HBM): 2458 kept rows of 4096 x
 // 22016, one token, 17.3 us for a given list (35 MB: 2.0 TB/s) and 22.4 with
-// the Top-K before it; 8295 of 13824 x 5120, 16 tokens, 31.3 us with the operand
+// the Top-K before it; 8295 of 13824 x 5120, 16 tokens, 30.8 us with the operand
 // kernel (39 MB: 1.2 TB/s).  One token is bound by the chain before the first block (scanning the list about 2.5 us, packing 1.5) and
 // then by issue, about 250 instructions a block; 16 tokens by the rate of
 // mma.sync, 128 of them a block at about 2.1 clocks and SM: 17 us.
@@ -520,8 +520,9 @@ constexpr int kPThreads = 1024;
 
 // The CTAs of a token each scatter the entries of the kept list that fall
 // into their range of rows into shared memory, then write the range as a
-// dense fp32 row (coef) or as the token's operand.
-constexpr int kCoefParts = 4;
+// dense fp32 row (coef) or as the token's operand.  (Four CTAs: 31.4 us for 16
+// tokens of 13824 x 5120 with the product, eight 30.8.)
+constexpr int kCoefParts = 8;
 
 __global__ void __launch_bounds__(kPThreads, 1)
     mx4_coef_kernel(const int32_t* __restrict__ idx, const float* __restrict__ val, int K, int d, float* coef,
