@@ -98,8 +98,11 @@ struct Layout {
   size_t partials = 0;
   size_t coef = 0, urows = 0, ucount = 0;
   size_t coef_hl = 0;  // M > 1: the coefficients' bf16 head and tail for the tensor-core GEMV
-  size_t mx4 = 0;      // the 4-bit sparse linear's coefficients (d_in a multiple of its block)
   size_t total = 0;
+  // the 4-bit sparse linear's coefficients and partial sums, and the bytes its
+  // calls need (sizes that suit the format; the other calls' total is not
+  // theirs: none of their intermediates but the kept lists is alive beside it)
+  size_t mx4 = 0, mx4_total = 0;
   bool list_gemv = false;  // M = 1: the row-streaming GEMV over a list of up to d_in rows fits
 };
 
@@ -180,6 +183,10 @@ int make_layout_uncached(int M, int d_in, int d_out, int K, Layout* L) {
   L->idx = take((size_t)M * K * 4);
   L->val = take((size_t)M * K * 4);
   L->nnz = take((size_t)M * 4);
+  if (d_in % LAROSA_MX4_BLOCK == 0 && d_out % LAROSA_MX4_BLOCK == 0) {
+    L->mx4 = off;
+    L->mx4_total = align_up(off + larosa::mx4_rows_buffer_bytes(M, d_in, d_out), 256);
+  }
   L->partials = take(partials * 4);
   if (M > 1) {
     L->coef = take((size_t)M * d_in * 4);
@@ -187,7 +194,6 @@ int make_layout_uncached(int M, int d_in, int d_out, int K, Layout* L) {
     L->ucount = take(4);
     L->coef_hl = take((size_t)2 * M * d_in * 2);  // the tensor-core path's coefficient rows
   }
-  if (d_in % LAROSA_MX4_BLOCK == 0 && d_out % LAROSA_MX4_BLOCK == 0) L->mx4 = take(larosa::mx4_rows_buffer_bytes(M, d_in, d_out));
   L->total = off;
   return LAROSA_OK;
 }
@@ -202,9 +208,8 @@ int check_sizes(int M, int d_in, int d_out, int K) {
 
 unsigned char* at(void* ws, size_t off) { return static_cast<unsigned char*>(ws) + off; }
 
-int workspace_ok(void* ws, size_t ws_bytes, const Layout& L) {
-  if (ws == nullptr || !aligned16(ws) || ws_bytes < L.total) return LAROSA_ERR_WORKSPACE;
-  return LAROSA_OK;
+int workspace_ok(void* ws, size_t ws_bytes, size_t need) {
+  return ws == nullptr || !aligned16(ws) || ws_bytes < need ? LAROSA_ERR_WORKSPACE : LAROSA_OK;
 }
 
 // Row-dot operands: rows of n_in elements, n_in a multiple of 8.
@@ -486,7 +491,7 @@ size_t larosa_workspace_bytes(int M, int d_in, int d_out, int K) {
   if (check_sizes(M, d_in, d_out, K) != LAROSA_OK) return 0;
   Layout L;
   if (make_layout(M, d_in, d_out, K, &L) != LAROSA_OK) return 0;
-  return L.total;
+  return std::max(L.total, L.mx4_total);
 }
 
 int larosa_workspace_layout(int M, int d_in, int d_out, int K, size_t* x_rot_offset,
@@ -602,7 +607,7 @@ int larosa_rotate_topk(const void* x, const void* Qt, float* x_rot, int32_t* idx
   Layout L;
   st = make_layout(1, d, 1, K, &L);
   if (st != LAROSA_OK) return st;
-  st = workspace_ok(ws, ws_bytes, L);
+  st = workspace_ok(ws, ws_bytes, L.total);
   if (st != LAROSA_OK) return st;
   larosa::RotSelArgs r;
   r.x = x;
@@ -631,7 +636,7 @@ int larosa_sparse_linear(const int32_t* idx, const float* val, int M, int K, con
   Layout L;
   st = make_layout(M, d_in, d_out, K, &L);
   if (st != LAROSA_OK) return st;
-  st = workspace_ok(ws, ws_bytes, L);
+  st = workspace_ok(ws, ws_bytes, L.total);
   if (st != LAROSA_OK) return st;
   st = debug_check_lists(idx, val, M, K, d_in, false, dev_status, reinterpret_cast<cudaStream_t>(stream));
   if (st != LAROSA_OK) return st;
@@ -652,7 +657,7 @@ static int rotate_topk_linear_impl(const void* x, const void* Qt, const void* W_
   Layout L;
   st = make_layout(M, d_in, d_out, K, &L);
   if (st != LAROSA_OK) return st;
-  st = workspace_ok(ws, ws_bytes, L);
+  st = workspace_ok(ws, ws_bytes, L.total);
   if (st != LAROSA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   float* x_rot = reinterpret_cast<float*>(at(ws, L.x_rot));
@@ -762,7 +767,7 @@ static int topk_linear_impl(const float* x_rot, const void* W_rot, int M, int d_
   Layout L;
   st = make_layout(M, d_in, d_out, K, &L);
   if (st != LAROSA_OK) return st;
-  st = workspace_ok(ws, ws_bytes, L);
+  st = workspace_ok(ws, ws_bytes, L.total);
   if (st != LAROSA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int32_t* idx = reinterpret_cast<int32_t*>(at(ws, L.idx));
@@ -810,7 +815,7 @@ int larosa_rotate_threshold_linear(const void* x, const void* Qt, const void* W_
   Layout L;
   st = make_layout(M, d_in, d_out, d_in, &L);
   if (st != LAROSA_OK) return st;
-  st = workspace_ok(ws, ws_bytes, L);
+  st = workspace_ok(ws, ws_bytes, L.total);
   if (st != LAROSA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   float* x_rot = reinterpret_cast<float*>(at(ws, L.x_rot));
@@ -1083,7 +1088,7 @@ int larosa_mx4_sparse_linear(const int32_t* idx, const float* val, int M, int K,
   Layout L;
   st = make_layout(M, d_in, d_out, K, &L);
   if (st != LAROSA_OK) return st;
-  st = workspace_ok(ws, ws_bytes, L);
+  st = workspace_ok(ws, ws_bytes, L.mx4_total);
   if (st != LAROSA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = debug_check_lists(idx, val, M, K, d_in, false, dev_status, s);
@@ -1110,7 +1115,7 @@ int larosa_mx4_topk_linear(const float* x_rot, const void* W_codes, const void* 
   Layout L;
   st = make_layout(M, d_in, d_out, K, &L);
   if (st != LAROSA_OK) return st;
-  st = workspace_ok(ws, ws_bytes, L);
+  st = workspace_ok(ws, ws_bytes, L.mx4_total);
   if (st != LAROSA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int32_t* idx = reinterpret_cast<int32_t*>(at(ws, L.idx));

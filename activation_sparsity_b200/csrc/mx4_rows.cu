@@ -600,16 +600,40 @@ cudaError_t allow_smem(F* fn, size_t bytes, int (&done)[64]) {
   return cudaSuccess;
 }
 
+// Whether a CTA takes 256 columns (two warps abreast): from 5 tokens on, and
+// for fewer where that still gives every SM its CTAs.
+bool wide_tiles(int M, int d_out) {
+  return mx4_rows_take_operand(M) || (d_out + 255) / 256 * kMaxSplits >= kFewCtas * 148;
+}
+
+// The column tiles of a product and the splits of each, from the sizes alone:
+// the launch and the size of the partial sums' buffer both go by it.
+struct RowsPlan {
+  int tiles, splits, blocks_per_split;
+  int tile_cols;
+};
+
+RowsPlan rows_plan(int M, int d_in, int d_out, bool list) {
+  const int halves = wide_tiles(M, d_out) ? 2 : 1;
+  const int warps = M <= 8 ? kRWarps : ManyCfg<2>::kWarps;
+  const int ctas = M <= 4 ? kFewCtas : M <= 8 ? ManyCfg<1>::kCtas : ManyCfg<2>::kCtas;
+  const int n_blocks = d_in / mx4::kBlock;
+  RowsPlan pl;
+  pl.tile_cols = 128 * halves;
+  pl.tiles = (d_out + pl.tile_cols - 1) / pl.tile_cols;
+  pl.splits = pick_splits(pl.tiles, n_blocks, warps / halves, ctas * 148);
+  if (list)  // the split's coefficients are staged in shared memory
+    while (((n_blocks + pl.splits - 1) / pl.splits) * 32 > kMaxSplitRows) ++pl.splits;
+  pl.blocks_per_split = (n_blocks + pl.splits - 1) / pl.splits;
+  return pl;
+}
+
 template <typename F>
-cudaError_t launch_tiles(F* fn, RParams p, int halves, int warps, int slots, size_t smem, cudaStream_t stream) {
-  const int tiles = (p.d_out + 128 * halves - 1) / (128 * halves);
-  const int n_blocks = p.d_in / mx4::kBlock;
-  int S = pick_splits(tiles, n_blocks, warps / halves, slots);
-  if (p.idx != nullptr) {  // the split's coefficients are staged in shared memory
-    while (((n_blocks + S - 1) / S) * 32 > kMaxSplitRows) ++S;
-    smem += (size_t)((n_blocks + S - 1) / S) * 32 * 4;
-  }
-  p.blocks_per_split = (n_blocks + S - 1) / S;
+cudaError_t launch_tiles(F* fn, RParams p, int warps, size_t smem, cudaStream_t stream) {
+  const RowsPlan pl = rows_plan(p.M, p.d_in, p.d_out, p.idx != nullptr);
+  p.blocks_per_split = pl.blocks_per_split;
+  if (p.idx != nullptr) smem += (size_t)pl.blocks_per_split * 32 * 4;
+  const int S = pl.splits, tiles = pl.tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S, tiles, 1);
   cfg.blockDim = dim3(32 * warps, 1, 1);
@@ -630,14 +654,12 @@ cudaError_t launch_few(const RParams& p, cudaStream_t stream) {
   auto* fn = mx4_rows_few_kernel<kList, kM, kHalves>;
   const cudaError_t e = allow_smem(fn, kBytes + (kList ? (size_t)kMaxSplitRows * 4 : 0), done);
   if (e != cudaSuccess) return e;
-  return launch_tiles(fn, p, kHalves, kRWarps, kFewCtas * 148, kBytes, stream);
+  return launch_tiles(fn, p, kRWarps, kBytes, stream);
 }
 
-// 256 columns per CTA where that still gives every SM its CTAs.
 template <bool kList, int kM>
 cudaError_t launch_few(const RParams& p, cudaStream_t stream) {
-  const bool wide = (p.d_out + 255) / 256 * kMaxSplits >= kFewCtas * 148;
-  return wide ? launch_few<kList, kM, 2>(p, stream) : launch_few<kList, kM, 1>(p, stream);
+  return wide_tiles(p.M, p.d_out) ? launch_few<kList, kM, 2>(p, stream) : launch_few<kList, kM, 1>(p, stream);
 }
 
 template <int O>
@@ -646,7 +668,7 @@ cudaError_t launch_many(const RParams& p, cudaStream_t stream) {
   static int done[64] = {0};
   cudaError_t e = allow_smem(mx4_rows_many_kernel<O>, C::kBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_tiles(mx4_rows_many_kernel<O>, p, 2, C::kWarps, C::kCtas * 148, C::kBytes, stream);
+  return launch_tiles(mx4_rows_many_kernel<O>, p, C::kWarps, C::kBytes, stream);
 }
 
 // Octets of tokens an operand is laid out for (1 to 4 tokens use none).
@@ -677,7 +699,13 @@ size_t coef_bytes(int M, int d_in) {
 }  // namespace
 
 size_t mx4_rows_buffer_bytes(int M, int d_in, int d_out) {
-  return coef_bytes(M, d_in) + (size_t)kMaxSplits * M * ((d_out + 255) / 256 * 256) * 4;
+  size_t partials = 0;  // of a single split: none
+  for (bool list : {false, true}) {
+    if (list && M != 1) break;  // only one token's list is read by the product
+    const RowsPlan pl = rows_plan(M, d_in, d_out, list);
+    if (pl.splits > 1) partials = std::max(partials, (size_t)pl.splits * pl.tiles * M * pl.tile_cols * 4);
+  }
+  return coef_bytes(M, d_in) + partials;
 }
 
 mx4::Operand mx4_rows_operand(void* buf, int M, int d_in) {
