@@ -25,7 +25,8 @@ __device__ __forceinline__ void piece_scale(unsigned top, float* up, float* down
   *down = __uint_as_float(static_cast<unsigned>(127 - 14 + min(e, 127)) << 23);
 }
 
-// v = p0 + 2^-11 p1 with two f16 pieces (|v| < 2^16).  A NaN or Inf gives NaN.
+// v = p0 + 2^-11 p1 with two f16 pieces (|v| < 2^16), to 2^-23 of v or 2^-36.  A
+// NaN or Inf gives NaN.
 __device__ __forceinline__ void split_pieces(float v, __half* p0, __half* p1) {
   *p0 = __float2half_rn(v);
   *p1 = __float2half_rn((v - __half2float(*p0)) * 2048.f);

@@ -21,8 +21,10 @@
 //     that the A operand wants, so no value is moved after its conversion;
 //   * a token's 32 coefficients of a block are divided by a power of two that
 //     puts the largest in [2^14, 2^15) and split into two f16 pieces of 11
-//     bits, v = (p0 + 2^-11 p1) 2^(e - 14): |error| <= 2^-24 |v| for entries
-//     within 2^-29 of the block's largest (below, 2^-50 of the largest).  The
+//     bits, v = (p0 + 2^-11 p1) 2^(e - 14): what p0 leaves has up to 12 bits,
+//     so |error| <= 2^-23 |v| for entries within 2^-27 of the block's largest
+//     (below, 2^-50 of the largest); a third piece for the last bit would take
+//     half as many MMAs again.  The
 //     pieces are neighbouring columns of the B operand: 4 tokens x 2 pieces
 //     fill its 8 columns;
 //   * a block's product is a fresh accumulator, scaled by the two powers of

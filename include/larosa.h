@@ -463,13 +463,17 @@ size_t larosa_mx4_linear_workspace_bytes(int M, int d_in, int d_out);
  * that some token keeps are read.  idx/val as for larosa_sparse_linear (each
  * token's indices distinct, in any order; an index that a token names twice
  * takes one of the two values, the debug checks report it); fp32
- * accumulation, with the coefficients exact to 2^-24 of themselves (2^-50 of
- * the largest of their token within the 32 rows of a block); finite
- * coefficients below 2^100 in magnitude.  An index outside [0, d_in) sets
- * LAROSA_DEV_INDEX and contributes nothing.  d_in and d_out multiples of 32;
- * W_codes, W_scales and y 16-byte aligned.  y: [M x d_out] fp32; results
- * repeat bit for bit.  ws: at least larosa_workspace_bytes(M, d_in, d_out, K)
- * bytes (it holds the tokens' coefficients between the call's two kernels).
+ * accumulation, with a coefficient held to 2^-23 of itself, or to 2^-50 of the
+ * largest of its token within the 32 rows of a block where that is more
+ * (2^-150 where that largest lies below 2^-100); finite coefficients below
+ * 2^100 in magnitude.  A NaN or Inf among a token's coefficients makes that
+ * token's outputs NaN and no other's.  A block with scale 255 of which some
+ * token keeps a row makes its column NaN for every token of the call.  An index
+ * outside [0, d_in) sets LAROSA_DEV_INDEX and contributes nothing.  d_in and
+ * d_out multiples of 32; W_codes, W_scales and y 16-byte aligned.  y:
+ * [M x d_out] fp32; results repeat bit for bit.  ws: at least
+ * larosa_workspace_bytes(M, d_in, d_out, K) bytes (it holds the tokens'
+ * coefficients between the call's two kernels).
  */
 int larosa_mx4_sparse_linear(const int32_t *idx, const float *val, int M,
                              int K, const void *W_codes, const void *W_scales,
@@ -503,8 +507,10 @@ int larosa_mx4_topk_linear(const float *x_rot, const void *W_codes,
  * 4-bit codes with scales S_gu and S_d (larosa_mx4_quantize with axis 0 of the
  * E d x 2 f and the E f x d matrix), d and f multiples of 32.  y: [M x d] fp32;
  * idx: [M x k] int32 and gate: [M x k] fp32, each may be NULL.  Scores are
- * summed in fp64, everything else in fp32; results repeat bit for bit.  Only
- * the chosen experts' weights are read.
+ * summed in fp64, everything else in fp32; for 4-bit experts x and h are held
+ * like the coefficients of larosa_mx4_sparse_linear (2^-23 of themselves or
+ * 2^-50 of the largest of their 32, below 2^100 in magnitude).  Results repeat
+ * bit for bit.  Only the chosen experts' weights are read.
  * 1 <= M <= LAROSA_MAX_M, d and f multiples of 8, at most LAROSA_MAX_D,
  * 1 <= k <= E, E <= LAROSA_MOE_MAX_E, k <= LAROSA_MOE_MAX_K; pointers 16-byte
  * aligned.  A NaN or Inf among the scores sets LAROSA_DEV_NONFINITE; that
