@@ -677,6 +677,9 @@ def larosa_mx4_quantize(src: torch.Tensor, axis: int = 1, codes: torch.Tensor | 
 
 def _mx4_pair(codes: torch.Tensor, scales: torch.Tensor, axis: int, what: str) -> tuple[int, int, int]:
     """Checks a (codes, scales) pair; returns its (rows, cols, device number)."""
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)):
+        _need(codes, what + "codes")
+        _need(scales, what + "scales")
     dev = codes.get_device()
     shape = codes.shape
     if (dev >= 0 and len(shape) == 2 and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
