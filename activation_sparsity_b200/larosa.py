@@ -152,28 +152,28 @@ class Workspace:
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
             else torch.device(device)
         self.buf = torch.zeros(0, dtype=torch.uint8, device=self.device)
-        self._need: dict[tuple[int, ...], int] = {}  # by the call's sizes
+        self._need: dict[tuple, int] = {}  # by the name of the size query and its arguments
 
     def get(self, M: int, d_in: int, d_out: int, K: int) -> torch.Tensor:
-        return self._sized(_lib.larosa_workspace_bytes, "larosa_workspace_bytes", (M, d_in, d_out, K))
+        return self._sized(("larosa_workspace_bytes", M, d_in, d_out, K))
 
     def get_mx4_linear(self, M: int, d_in: int, d_out: int) -> torch.Tensor:
         """The buffer for larosa_mx4_linear of these sizes."""
-        return self._sized(_lib.larosa_mx4_linear_workspace_bytes, "larosa_mx4_linear_workspace_bytes",
-                           (M, d_in, d_out))
+        return self._sized(("larosa_mx4_linear_workspace_bytes", M, d_in, d_out))
 
     def get_moe(self, M: int, d: int, f: int, E: int, k: int) -> torch.Tensor:
         """The buffer for larosa_moe_layer of these sizes."""
-        return self._sized(_lib.larosa_moe_workspace_bytes, "larosa_moe_workspace_bytes", (M, d, f, E, k))
+        return self._sized(("larosa_moe_workspace_bytes", M, d, f, E, k))
 
-    def _sized(self, query, name: str, key: tuple) -> torch.Tensor:
-        need = self._need.get(key)  # the entry points differ in the number of sizes
+    def _sized(self, query: tuple) -> torch.Tensor:
+        """The buffer for a size query: the name of the library's function, then its arguments."""
+        need = self._need.get(query)
         if need is None:
             with torch.cuda.device(self.device):
-                need = int(query(*key))
+                need = int(getattr(_lib, query[0])(*query[1:]))
             if need == 0:
-                raise LarosaError(2, name)
-            self._need[key] = need
+                raise LarosaError(2, query[0])
+            self._need[query] = need
         if self.buf.numel() < need:
             self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return self.buf
@@ -609,9 +609,9 @@ def _status_word(dev_status: torch.Tensor | None, dev: int) -> int:
     return dev_status.data_ptr()
 
 
-def _ws_pair(ws, dev: int, sizes: tuple) -> tuple[int, int]:
-    """(address, bytes) of a workspace for these sizes; ws: a Workspace, a
-    tensor, or None for the current stream's own."""
+def _ws_pair(ws, dev: int, query: tuple) -> tuple[int, int]:
+    """(address, bytes) of a workspace for a size query (see Workspace._sized);
+    ws: a Workspace, a tensor, or None for the current stream's own."""
     if ws is None:
         ws = _ws_cache.get((dev, _raw_stream(dev)))
         if ws is None:
@@ -619,9 +619,9 @@ def _ws_pair(ws, dev: int, sizes: tuple) -> tuple[int, int]:
     if isinstance(ws, Workspace):
         buf = ws.buf
         n = buf.numel()  # of bytes
-        need = ws._need.get(sizes)
+        need = ws._need.get(query)
         if need is None or n < need:
-            buf = (ws.get if len(sizes) == 4 else ws.get_moe if len(sizes) == 5 else ws.get_mx4_linear)(*sizes)
+            buf = ws._sized(query)
             n = buf.numel()
     else:
         buf = ws
@@ -734,7 +734,7 @@ def larosa_mx4_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, Wt_codes: t
         y = torch.empty(M, d_out, dtype=dtype, device=Wt_codes.device)
     else:
         _need_out(y, "y", (M, d_out), y.dtype, dev)
-    p, n = _ws_pair(ws, dev, (M, d_in, d_out))
+    p, n = _ws_pair(ws, dev, ("larosa_mx4_linear_workspace_bytes", M, d_in, d_out))
     _call("larosa_mx4_linear", dev, _lib.larosa_mx4_linear,
           (x_codes.data_ptr(), x_scales.data_ptr(), Wt_codes.data_ptr(), Wt_scales.data_ptr(), M, d_in, d_out,
            y.data_ptr(), p, n, _status_word(dev_status, dev), _dtype_code(y)))
@@ -757,7 +757,7 @@ def larosa_mx4_sparse_linear(idx: torch.Tensor, val: torch.Tensor, W_codes: torc
         y = torch.empty(M, d_out, dtype=torch.float32, device=W_codes.device)
     else:
         _need_out(y, "y", (M, d_out), torch.float32, dev)
-    p, n = _ws_pair(ws, dev, (M, d_in, d_out, K))
+    p, n = _ws_pair(ws, dev, ("larosa_workspace_bytes", M, d_in, d_out, K))
     _call("larosa_mx4_sparse_linear", dev, _lib.larosa_mx4_sparse_linear,
           (idx.data_ptr(), val.data_ptr(), M, K, W_codes.data_ptr(), W_scales.data_ptr(), d_in, d_out, y.data_ptr(),
            p, n, _status_word(dev_status, dev)))
@@ -779,7 +779,7 @@ def larosa_mx4_topk_linear(x_rot: torch.Tensor, W_codes: torch.Tensor, W_scales:
         y = torch.empty(M, d_out, dtype=torch.float32, device=W_codes.device)
     else:
         _need_out(y, "y", (M, d_out), torch.float32, dev)
-    p, n = _ws_pair(ws, dev, (M, d_in, d_out, K))
+    p, n = _ws_pair(ws, dev, ("larosa_workspace_bytes", M, d_in, d_out, K))
     _call("larosa_mx4_topk_linear", dev, _lib.larosa_mx4_topk_linear,
           (x_rot.data_ptr(), W_codes.data_ptr(), W_scales.data_ptr(), M, d_in, d_out, K, y.data_ptr(), p, n,
            _status_word(dev_status, dev)))
@@ -827,7 +827,7 @@ def larosa_moe_layer(x: torch.Tensor, Wr: torch.Tensor, W_gu: torch.Tensor, W_d:
         sg, sd = S_gu.data_ptr(), S_d.data_ptr()
     if not ok or Wr.shape != (E, d):
         raise ValueError("shapes of x, Wr, the experts and their scales do not agree")
-    p, n = _ws_pair(ws, dev, (M, d, f, E, k))
+    p, n = _ws_pair(ws, dev, ("larosa_moe_workspace_bytes", M, d, f, E, k))
     if y is None:
         y = torch.empty(M, d, dtype=torch.float32, device=device)
     else:

@@ -1,4 +1,6 @@
 """Arguments of the 4-bit and expert calls in Python: what is taken, what is refused."""
+from unittest import mock
+
 import pytest
 import torch
 
@@ -12,3 +14,18 @@ def test_what_is_no_tensor_is_refused_as_such():
                  lambda: L.larosa_mx4_quantize(None), lambda: L.larosa_moe_layer(None, t, t, t, 1)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_workspace_sizes_are_kept_apart_by_call():
+    """Two calls with the same number of sizes, and the same sizes, each get their own query."""
+    from activation_sparsity_b200 import larosa
+    ws = larosa.Workspace.__new__(larosa.Workspace)
+    ws.device, ws.buf, ws._need = torch.device("cuda", 0), torch.zeros(1000, dtype=torch.uint8), {}
+    lib = mock.Mock(first=lambda *a: 10 + len(a), second=lambda *a: 20 + len(a), none=lambda *a: 0)
+    lib.larosa_status_string.return_value = lib.larosa_last_error_string.return_value = b""
+    with mock.patch.object(torch.cuda, "device"), mock.patch.object(larosa, "_lib", lib):
+        for _ in range(2):
+            assert ws._sized(("first", 1, 2, 3)) is ws.buf and ws._sized(("second", 1, 2, 3)) is ws.buf
+        assert ws._need == {("first", 1, 2, 3): 13, ("second", 1, 2, 3): 23}
+        with pytest.raises(larosa.LarosaError):
+            ws._sized(("none", 1, 2, 3))
