@@ -657,9 +657,12 @@ def larosa_mx4_quantize(src: torch.Tensor, axis: int = 1, codes: torch.Tensor | 
     """A matrix (or a stack of matrices, [..., rows, cols]) in microscaled 4-bit
     form: (codes uint8 [..., rows, cols / 2], scales uint8).  axis 1: blocks of
     32 along a row, scales [..., rows, cols / 32]; axis 0: down a column, scales
-    [..., rows / 32, cols].  See larosa_mx4_quantize in the header."""
+    [..., rows / 32, cols].  A single token [d] is a row [1, d].  See
+    larosa_mx4_quantize in the header."""
     _need(src, "src")
     dev, device = src.get_device(), src.device
+    if src.dim() < 2:
+        src = _as2d(src)
     cs, ss, rows, cols = _mx4_shapes(src.shape, axis)
     if codes is None:
         codes = torch.empty(*cs, dtype=torch.uint8, device=device)  # a third faster than with one tuple

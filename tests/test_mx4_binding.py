@@ -29,3 +29,17 @@ def test_workspace_sizes_are_kept_apart_by_call():
         assert ws._need == {("first", 1, 2, 3): 13, ("second", 1, 2, 3): 23}
         with pytest.raises(larosa.LarosaError):
             ws._sized(("none", 1, 2, 3))
+
+
+@pytest.mark.gpu
+def test_a_single_token_may_have_one_dimension():
+    import activation_sparsity_b200 as L
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(96, dtype=dtype, device="cuda")
+        codes, scales = L.larosa_mx4_quantize(x)
+        c, s = L.larosa_mx4_quantize(x.view(1, 96))
+        assert codes.shape == (1, 48) and torch.equal(codes, c) and torch.equal(scales, s)
+        W = L.larosa_mx4_quantize(torch.randn(40, 96, device="cuda"))
+        assert L.larosa_mx4_linear(codes, scales, *W).shape == (1, 40)
+        with pytest.raises(ValueError):
+            L.larosa_mx4_quantize(x, axis=0)  # one row is no block
