@@ -590,6 +590,11 @@ def _need_out(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, dev:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _need_typed(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype | None, dev: int) -> None:
+    """A given output whose type the caller chooses, by `dtype` or (None) by the output itself."""
+    _need_out(t, name, shape, getattr(t, "dtype", None) if dtype is None else dtype, dev)
+
+
 def _call(where: str, dev: int, fn, args: tuple) -> None:
     """fn(*args, stream) on device `dev`, on its current stream."""
     if _current_device() == dev:
@@ -705,13 +710,14 @@ def _mx4_pair(codes: torch.Tensor, scales: torch.Tensor, axis: int, what: str) -
 
 
 def larosa_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, axis: int = 1,
-                          dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
-    """The values that codes and scales (larosa_mx4_quantize) stand for."""
+                          dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that codes and scales (larosa_mx4_quantize) stand for, in `dtype`
+    (None: out's, or fp32)."""
     rows, cols, dev = _mx4_pair(codes, scales, axis, "")
     if out is None:
-        out = torch.empty(*codes.shape[:-1], cols, dtype=dtype, device=codes.device)
+        out = torch.empty(*codes.shape[:-1], cols, dtype=dtype or torch.float32, device=codes.device)
     else:
-        _need_out(out, "out", (*codes.shape[:-1], cols), out.dtype, dev)
+        _need_typed(out, "out", (*codes.shape[:-1], cols), dtype, dev)
     _call("larosa_mx4_dequantize", dev, _lib.larosa_mx4_dequantize,
           (codes.data_ptr(), scales.data_ptr(), rows, cols, axis, _dtype_code(out), out.data_ptr()))
     return out
@@ -722,11 +728,11 @@ def larosa_mx4_linear_workspace_bytes(M: int, d_in: int, d_out: int) -> int:
 
 
 def larosa_mx4_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, Wt_codes: torch.Tensor,
-                      Wt_scales: torch.Tensor, dtype: torch.dtype = torch.float32, y: torch.Tensor | None = None,
+                      Wt_scales: torch.Tensor, dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
                       ws=None, dev_status: torch.Tensor | None = None) -> torch.Tensor:
-    """y = x . W of two 4-bit matrices, [M, d_out] in `dtype`: x [M, d_in] and the
-    weight in torch.nn.Linear layout [d_out, d_in], both of larosa_mx4_quantize
-    with axis 1."""
+    """y = x . W of two 4-bit matrices, [M, d_out] in `dtype` (None: y's, or fp32):
+    x [M, d_in] and the weight in torch.nn.Linear layout [d_out, d_in], both of
+    larosa_mx4_quantize with axis 1."""
     M, d_in, x_dev = _mx4_pair(x_codes, x_scales, 1, "x_")
     d_out, d_w, dev = _mx4_pair(Wt_codes, Wt_scales, 1, "Wt_")
     if d_w != d_in or x_codes.dim() != 2 or Wt_codes.dim() != 2:
@@ -734,9 +740,9 @@ def larosa_mx4_linear(x_codes: torch.Tensor, x_scales: torch.Tensor, Wt_codes: t
     if x_dev != dev:
         raise ValueError(f"x_codes is on {x_codes.device}, the other tensors are on cuda:{dev}")
     if y is None:
-        y = torch.empty(M, d_out, dtype=dtype, device=Wt_codes.device)
+        y = torch.empty(M, d_out, dtype=dtype or torch.float32, device=Wt_codes.device)
     else:
-        _need_out(y, "y", (M, d_out), y.dtype, dev)
+        _need_typed(y, "y", (M, d_out), dtype, dev)
     p, n = _ws_pair(ws, dev, ("larosa_mx4_linear_workspace_bytes", M, d_in, d_out))
     _call("larosa_mx4_linear", dev, _lib.larosa_mx4_linear,
           (x_codes.data_ptr(), x_scales.data_ptr(), Wt_codes.data_ptr(), Wt_scales.data_ptr(), M, d_in, d_out,

@@ -43,3 +43,24 @@ def test_a_single_token_may_have_one_dimension():
         assert L.larosa_mx4_linear(codes, scales, *W).shape == (1, 40)
         with pytest.raises(ValueError):
             L.larosa_mx4_quantize(x, axis=0)  # one row is no block
+
+
+@pytest.mark.gpu
+def test_an_output_of_another_type_than_asked_for_is_refused():
+    import activation_sparsity_b200 as L
+    f32, bf16 = torch.float32, torch.bfloat16
+    x = L.larosa_mx4_quantize(torch.randn(3, 64, device="cuda"))
+    W = L.larosa_mx4_quantize(torch.randn(16, 64, device="cuda"))
+    for asked, given in ((f32, bf16), (bf16, f32)):
+        y = torch.zeros(3, 16, dtype=given, device="cuda")
+        with pytest.raises(TypeError):
+            L.larosa_mx4_linear(*x, *W, dtype=asked, y=y)
+        out = torch.zeros(3, 64, dtype=given, device="cuda")
+        with pytest.raises(TypeError):
+            L.larosa_mx4_dequantize(*x, dtype=asked, out=out)
+        assert not y.any() and not out.any()
+        assert L.larosa_mx4_linear(*x, *W, dtype=given, y=y) is y
+        assert L.larosa_mx4_linear(*x, *W, y=y) is y  # without a type: y's
+        assert L.larosa_mx4_dequantize(*x, out=out) is out
+        assert L.larosa_mx4_linear(*x, *W, dtype=asked).dtype == asked
+    assert L.larosa_mx4_linear(*x, *W).dtype == f32 and L.larosa_mx4_dequantize(*x).dtype == f32
