@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (it >= n_it || !ok) break;
         const int s = it % C::kStages;
         if (it >= C::kStages) {
-          ok = mbar_wait_bounded(&empty[s], ((it / C::kStages) - 1) & 1, abort_flag, p.wait_ns);
+          ok = mx4::wait_bounded<1>(&empty[s], ((it / C::kStages) - 1) & 1, abort_flag, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
             *abort_flag = 1;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     if (lane == 0) {
       for (int it = 0; it < n_it; ++it) {
         const int s = it % C::kStages;
-        if (it >= C::kStages && !mbar_wait_bounded(&empty[s], ((it / C::kStages) - 1) & 1, abort_flag, p.wait_ns)) {
+        if (it >= C::kStages && !mx4::wait_bounded<1>(&empty[s], ((it / C::kStages) - 1) & 1, abort_flag, p.wait_ns)) {
           *abort_flag = 1;
           break;
         }
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     if (lane == 0) {
       for (int it = 0; it < n_it; ++it) {
         const int s = it % C::kStages;
-        if (!mbar_wait_bounded(&full[s], (it / C::kStages) & 1, abort_flag, p.wait_ns)) {
+        if (!mx4::wait_bounded<1>(&full[s], (it / C::kStages) & 1, abort_flag, p.wait_ns)) {
           *abort_flag = 1;
           break;
         }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
   __syncwarp();
 
   // ------------------------------------------------------------------ epilogue
-  const bool finished = mbar_wait_bounded(&done, 0, nullptr, p.wait_ns);
+  const bool finished = mx4::wait_bounded<1>(&done, 0, nullptr, p.wait_ns);
   tc::tmem_fence_after();
   __syncwarp();  // tcgen05.ld is .aligned: the whole warp issues it together
   if (!finished) *abort_flag = 1;
@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
     // let the MMAs and every copy this CTA armed end before its memory goes
     // away; a stage whose scales never came cannot complete and takes the whole
     // time
-    mbar_wait_bounded(&done, 0, nullptr, mx4::kSettleNs);
+    mx4::wait_bounded<1>(&done, 0, nullptr, mx4::kSettleNs);
     for (int it = max(0, issued - C::kStages); it < issued; ++it)
-      mbar_wait_bounded(&full[it % C::kStages], (it / C::kStages) & 1, nullptr, mx4::kSettleNs);
+      mx4::wait_bounded<1>(&full[it % C::kStages], (it / C::kStages) & 1, nullptr, mx4::kSettleNs);
     report(p.dev_status, LAROSA_DEV_TIMEOUT);
   }
   __syncthreads();

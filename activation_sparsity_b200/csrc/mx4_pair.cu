@@ -108,7 +108,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           unsigned long long limit_ns) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, abort, limit_ns);
+  if ((threadIdx.x & 31) == 0) ok = mx4::wait_bounded<16>(bar, parity, abort, limit_ns);
   return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
 }
 
@@ -325,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       for (int tile = pair; tile < p.tiles && ok; tile += pairs) {
         const int n0 = tile % p.tn * NT, j0 = tile / p.tn * 256;
         for (int it = 0; it < n_it; ++it) {
-          if (use > 0 && !mbar_wait_bounded(&empty[s], (uint32_t)(use - 1) & 1u, abort_flag, p.wait_ns)) {
+          if (use > 0 && !mx4::wait_bounded<16>(&empty[s], (uint32_t)(use - 1) & 1u, abort_flag, p.wait_ns)) {
             *abort_flag = 1;
             ok = false;
             break;
@@ -350,13 +350,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       for (int tile = pair; tile < p.tiles && ok; tile += pairs, ++round) {
         const int acc = round % C::kAcc;
         if (round >= C::kAcc &&
-            !mbar_wait_bounded(&acc_empty[acc], (uint32_t)(round / C::kAcc - 1) & 1u, abort_flag, p.wait_ns)) {
+            !mx4::wait_bounded<16>(&acc_empty[acc], (uint32_t)(round / C::kAcc - 1) & 1u, abort_flag, p.wait_ns)) {
           *abort_flag = 1;
           break;
         }
         tc::tmem_fence_after();
         for (int it = 0; it < n_it; ++it) {
-          if (!mbar_wait_bounded(&full[s], (uint32_t)use & 1u, abort_flag, p.wait_ns)) {
+          if (!mx4::wait_bounded<16>(&full[s], (uint32_t)use & 1u, abort_flag, p.wait_ns)) {
             *abort_flag = 1;
             ok = false;
             break;

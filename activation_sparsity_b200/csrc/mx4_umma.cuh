@@ -16,6 +16,22 @@ constexpr int kStageBlocks = kStageK / kBlock;
 // microseconds, and the limit may be as short as one.
 constexpr unsigned long long kSettleNs = 100000;
 
+// mbar_wait_bounded that looks at the clock and at *abort every kEvery tries: the
+// hardware holds a try for a fraction of a microsecond, so that the 256 tries
+// between two looks there outlast the shortest limits (at 1 us no wait of a
+// product of 3 tokens of 32768 x 20000 ran out; so every call's does).  One try for
+// the stages of few tokens, 12.0 us for 3 of 11008 x 4096 (12.1 with 256); 16 for the
+// pairs of SMs, 290.5 us for 4096 of 5120 x 27648 as with 256 (291.4 with one).
+template <uint32_t kEvery>
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                             unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
+    if (it % kEvery == 0 && ((abort != nullptr && *abort) || global_timer_ns() - t0 > limit_ns)) return false;
+  return true;
+}
+
 // Instruction descriptor of kind::mxf4: A and B e2m1 (1), K-major, scales
 // ue8m0, M = m, N = n; sf selects which half of a scale word the 64 inputs
 // take (0: bytes 0-1, 2: bytes 2-3).
