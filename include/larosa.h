@@ -518,8 +518,9 @@ int larosa_mx4_topk_linear(const float *x_rot, const void *W_codes,
  * ws: at least larosa_moe_workspace_bytes(M, d, f, E, k) bytes, zero-filled
  * before its first use; it holds counters that are zero between calls, so
  * calls sharing a workspace must not overlap.  A cooperative launch (every CTA
- * resident at once) whose grid waits for itself four times, each within the
- * wait limit (LAROSA_DEV_TIMEOUT beyond it).
+ * resident at once, as many as the SMs that the device reports hold; where that
+ * cannot be, LAROSA_ERR_CUDA) whose grid waits for itself four times, each
+ * within the wait limit (LAROSA_DEV_TIMEOUT beyond it).
  */
 int larosa_moe_layer(const void *x, const void *Wr, const void *W_gu,
                      const void *S_gu, const void *W_d, const void *S_d, int M,
@@ -591,8 +592,9 @@ int larosa_set_wait_limit_ns(uint64_t limit_ns, uint64_t *previous);
  * on).  While on, every call that takes or writes kept lists also launches
  * a check of them on the same stream, after (for lists the library writes:
  * larosa_topk, larosa_rotate_topk, larosa_rotate_topk_linear,
- * larosa_topk_linear) or before (for the caller's lists: larosa_sparse_linear,
- * larosa_sparse_linear_noalloc, larosa_sparse_lowrank_linear) the compute:
+ * larosa_topk_linear, larosa_mx4_topk_linear) or before (for the caller's
+ * lists: larosa_sparse_linear, larosa_sparse_linear_noalloc,
+ * larosa_sparse_lowrank_linear, larosa_mx4_sparse_linear) the compute:
  * each row's indices must lie in [0, d_in) (else LAROSA_DEV_INDEX), be
  * distinct and, where the library wrote them, ascending (else
  * LAROSA_DEV_LIST), and the values finite (else LAROSA_DEV_NONFINITE).
