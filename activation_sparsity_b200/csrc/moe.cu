@@ -53,7 +53,7 @@
 // Measured (B200, graph replay, weights from HBM): one token, 8 of 128 bf16
 // experts of 2048 to 768, 34.5 us (75 MB, 2.2 TB/s: 13 us outside the two
 // streams, which run at 3.6 TB/s); five tokens, 4 of 60 fp32 experts of 1024 to
-// 1408, 80 to 83 us (303 MB, 3.7 TB/s, from one placement of the weights to
+// 1408, 79 to 83 us (303 MB, 3.7 TB/s, from one placement of the weights to
 // another); 16 tokens, 2 of 8 4-bit experts of 4096 to 14336, 234 us (742 MB,
 // 3.2 TB/s: bound by issue and mma.sync, the same copies without the products
 // take 176 us); a layer of 8 bf16 experts of 256 to 512, 15.6 us, all of it the

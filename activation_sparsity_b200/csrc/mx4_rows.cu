@@ -62,11 +62,15 @@
 //                    keeps is replaced by one that is read anyway.
 //
 // Measured (B200, graph replay, weights from HBM): 2458 kept rows of 4096 x
-// 22016, one token, 17.3 us for a given list (35 MB: 2.0 TB/s) and 22.4 with
-// the Top-K before it; 8295 of 13824 x 5120, 16 tokens, 30.8 us with the operand
-// kernel (39 MB: 1.2 TB/s).  One token is bound by the chain before the first block (scanning the list about 2.5 us, packing 1.5) and
-// then by issue, about 250 instructions a block; 16 tokens by the rate of
-// mma.sync, 128 of them a block at about 2.1 clocks and SM: 17 us.
+// 22016, one token, 17.3 us for a given list (30 MB: 1.7 TB/s) and 22.4 with
+// the Top-K before it (4 tokens 22.9 and 28.3, 8 tokens 25.2 and 30.9, 16 tokens
+// 43.0 and 49.3); 8295 of 13824 x 5120, 16 tokens, 30.8 us with the operand kernel
+// (39 MB: 1.3 TB/s).  One token is bound by the chain before the first block
+// (scanning the list about 2.5 us, packing 1.5) and then by issue, about 250
+// instructions a block; 16 tokens by no rate alone: 64 mma.sync a block at about 2.1
+// clocks and SM are 8 us, its 550 instructions 9 us of issue, and three warps per
+// scheduler do not cover one another's waits; the operand kernel before takes 8 us by
+// itself, part of it beside the product's start.
 #include <algorithm>
 
 #include "common.cuh"
