@@ -140,12 +140,38 @@ def _need(t: torch.Tensor, name: str, dtype=None) -> None:
 
 # ------------------------------------------------------------------ workspace
 
+_cuda_driver = None
+
+
+def _capture_id(device: torch.device) -> int:
+    """The number of the capture that the device's current stream takes part in, 0 outside of one."""
+    global _cuda_driver
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            return 0
+    if _cuda_driver is None:
+        _cuda_driver = ctypes.CDLL("libcuda.so.1")
+    state, number = ctypes.c_int(0), ctypes.c_uint64(0)
+    status = _cuda_driver.cuStreamGetCaptureInfo_v2(_stream(device), ctypes.byref(state), ctypes.byref(number),
+                                                    None, None, None)
+    if status != 0:
+        raise RuntimeError(f"cuStreamGetCaptureInfo_v2: error {status}")
+    return number.value
+
+
 class Workspace:
     """A zero-initialised scratch buffer for one stream, grown on demand.
 
     The library leaves the counter words it uses at zero after every call, so
     the buffer is reused without clearing.  A buffer serves one stream at a
-    time; calls on different streams that may overlap need their own.
+    time; calls on different streams that may overlap need their own, and so do
+    graphs that may be replayed at the same time.
+
+    A captured graph goes on using the buffer it was captured with: one that
+    has been outgrown is kept (sizes at least double, so that together they are no
+    larger than the last).  A buffer that had to be made inside a capture is
+    zeroed by that graph, at every replay and at no other time, so nothing
+    outside of that capture uses it.
     """
 
     def __init__(self, device=None):
@@ -153,6 +179,8 @@ class Workspace:
             else torch.device(device)
         self.buf = torch.zeros(0, dtype=torch.uint8, device=self.device)
         self._need: dict[tuple, int] = {}  # by the name of the size query and its arguments
+        self._outgrown: list[torch.Tensor] = []
+        self._capture = 0  # the capture that buf was made in, 0: none
 
     def get(self, M: int, d_in: int, d_out: int, K: int) -> torch.Tensor:
         return self._sized(("larosa_workspace_bytes", M, d_in, d_out, K))
@@ -174,13 +202,24 @@ class Workspace:
             if need == 0:
                 raise LarosaError(2, query[0])
             self._need[query] = need
-        if self.buf.numel() < need:
-            self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        if self.buf.numel() < need or self._capture:
+            self._renew(need)
         return self.buf
 
+    def _renew(self, need: int) -> None:
+        """A buffer of at least `need` bytes that may be used where the caller is."""
+        capture, have = _capture_id(self.device), self.buf.numel()
+        if have >= need and capture == self._capture:
+            return
+        if have and not self._capture:  # (one made in a capture belongs to that graph's memory)
+            self._outgrown.append(self.buf)
+        self.buf = torch.zeros(have if have >= need else max(need, 2 * have), dtype=torch.uint8, device=self.device)
+        self._capture = capture
+
     def reset(self) -> None:
-        """Zero the buffer again (needed after a device-side error)."""
-        self.buf.zero_()
+        """Zero the buffer again, and those that graphs may still use (needed after a device-side error)."""
+        for buf in (*self._outgrown, self.buf):
+            buf.zero_()
 
 
 _ws_lock = threading.Lock()
@@ -625,7 +664,7 @@ def _ws_pair(ws, dev: int, query: tuple) -> tuple[int, int]:
         buf = ws.buf
         n = buf.numel()  # of bytes
         need = ws._need.get(query)
-        if need is None or n < need:
+        if need is None or n < need or ws._capture:
             buf = ws._sized(query)
             n = buf.numel()
     else:

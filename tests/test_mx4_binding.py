@@ -21,6 +21,7 @@ def test_workspace_sizes_are_kept_apart_by_call():
     from activation_sparsity_b200 import larosa
     ws = larosa.Workspace.__new__(larosa.Workspace)
     ws.device, ws.buf, ws._need = torch.device("cuda", 0), torch.zeros(1000, dtype=torch.uint8), {}
+    ws._outgrown, ws._capture = [], 0
     lib = mock.Mock(first=lambda *a: 10 + len(a), second=lambda *a: 20 + len(a), none=lambda *a: 0)
     lib.larosa_status_string.return_value = lib.larosa_last_error_string.return_value = b""
     with mock.patch.object(torch.cuda, "device"), mock.patch.object(larosa, "_lib", lib):
