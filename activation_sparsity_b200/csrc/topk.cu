@@ -12,6 +12,8 @@
 // scan that places every kept entry, ascending in the index.  The whole
 // vector (d <= 32768 fp32) stays in shared memory; nothing but the input row
 // and the K outputs touches global memory.
+#include <type_traits>
+
 #include "coef.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -40,14 +42,24 @@ __device__ __forceinline__ void write_head_tail(const uint32_t* bits, int d, Kep
       hi, lo);
 }
 
+// What the 4-bit sparse linear takes of a token: with op.piece != nullptr the
+// token's operand, else the fp32 row (x where kept, else 0; d a multiple of 32).
+struct Mx4Out {
+  float* coef;
+  mx4::Operand op;
+};
+// A kernel of its own for the other calls: with these outputs behind a test of
+// their pointers the Top-K of 1 to 16 short rows took 0.2 us longer (3.7 and 3.9 us
+// at d = 256).
+struct NoMx4Out {};
+
 // With hl != nullptr the kernel also writes each token's dense coefficient
 // rows for the tensor-core product: hl[m][0, d) the heads, hl[M + m][0, d)
-// the tails (d a multiple of 8); with coef != nullptr the fp32 row (x where
-// kept, else 0), and with op.piece != nullptr the token's operand of the
-// 4-bit sparse linear (d a multiple of 32).
+// the tails (d a multiple of 8).
+template <typename Out>
 __global__ void __launch_bounds__(kTopkThreads, 1)
     topk_kernel(const float* __restrict__ x_rot, int d, int K, int32_t* __restrict__ idx,
-                float* __restrict__ val, int* dev_status, __nv_bfloat16* hl, float* coef, mx4::Operand op) {
+                float* __restrict__ val, int* dev_status, __nv_bfloat16* hl, const Out out) {
   // raw fp32 bits of the row, padded with zero keys to a multiple of 4: a
   // zero key at an index >= d loses every tie, so padding is never kept
   extern __shared__ __align__(16) uint32_t bits[];
@@ -125,15 +137,18 @@ __global__ void __launch_bounds__(kTopkThreads, 1)
     write_head_tail(bits, d, [&](uint32_t key, int i) { return is_kept(key, i, e); }, hl + (size_t)m * d,
                     hl + (M + m) * d);
   }
-  auto kept_value = [&](int i) {
-    const uint32_t u = bits[i];
-    return is_kept(u & kKeyMask, i, e) ? __uint_as_float(u) : 0.f;
-  };
-  if (coef != nullptr)
-    for (int i = tid; i < d; i += kTopkThreads) coef[(size_t)m * d + i] = kept_value(i);
-  if (op.piece != nullptr)
-    for (int b = tid >> 5; b < d / mx4::kBlock; b += kTopkThreads / 32)
-      op.put(b, m, kept_value(b * 32 + (tid & 31)), tid & 31);
+  if constexpr (std::is_same_v<Out, Mx4Out>) {
+    auto kept_value = [&](int i) {
+      const uint32_t u = bits[i];
+      return is_kept(u & kKeyMask, i, e) ? __uint_as_float(u) : 0.f;
+    };
+    if (out.op.piece == nullptr) {
+      for (int i = tid; i < d; i += kTopkThreads) out.coef[(size_t)m * d + i] = kept_value(i);
+    } else {
+      for (int b = tid >> 5; b < d / mx4::kBlock; b += kTopkThreads / 32)
+        out.op.put(b, m, kept_value(b * 32 + (tid & 31)), tid & 31);
+    }
+  }
 }
 
 // The tokens' dense coefficient rows for the tensor-core sparse linear, from
@@ -276,16 +291,17 @@ cudaError_t launch_coef_rows(const int32_t* idx, const float* val, int M, int K,
   return cudaLaunchKernelEx(&cfg, coef_rows_kernel, idx, val, K, d, hl, dev_status);
 }
 
-cudaError_t launch_topk(const float* x_rot, int M, int d, int K, int32_t* idx, float* val,
-                        int* dev_status, cudaStream_t stream, __nv_bfloat16* hl, void* mx4_buf) {
-  if ((hl != nullptr && d % 8 != 0) || (mx4_buf != nullptr && d % mx4::kBlock != 0)) return cudaErrorInvalidValue;
+namespace {
+template <typename Out>
+cudaError_t launch_topk_out(const float* x_rot, int M, int d, int K, int32_t* idx, float* val, int* dev_status,
+                            cudaStream_t stream, __nv_bfloat16* hl, const Out& out) {
   const size_t smem = (size_t)((d + 3) & ~3) * sizeof(uint32_t);
   static int configured[64] = {0};  // per device: dynamic shared memory limit raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(topk_kernel<Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(LAROSA_MAX_D * sizeof(uint32_t)));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
@@ -300,10 +316,16 @@ cudaError_t launch_topk(const float* x_rot, int M, int d, int K, int32_t* idx, f
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const bool operand = mx4_buf != nullptr && mx4_rows_take_operand(M);
-  return cudaLaunchKernelEx(&cfg, topk_kernel, x_rot, d, K, idx, val, dev_status, hl,
-                            operand ? nullptr : static_cast<float*>(mx4_buf),
-                            operand ? mx4_rows_operand(mx4_buf, M, d) : mx4::Operand{});
+  return cudaLaunchKernelEx(&cfg, topk_kernel<Out>, x_rot, d, K, idx, val, dev_status, hl, out);
+}
+}  // namespace
+
+cudaError_t launch_topk(const float* x_rot, int M, int d, int K, int32_t* idx, float* val,
+                        int* dev_status, cudaStream_t stream, __nv_bfloat16* hl, void* mx4_buf) {
+  if ((hl != nullptr && d % 8 != 0) || (mx4_buf != nullptr && d % mx4::kBlock != 0)) return cudaErrorInvalidValue;
+  if (mx4_buf == nullptr) return launch_topk_out(x_rot, M, d, K, idx, val, dev_status, stream, hl, NoMx4Out{});
+  return launch_topk_out(x_rot, M, d, K, idx, val, dev_status, stream, hl,
+                         Mx4Out{static_cast<float*>(mx4_buf), mx4_rows_operand(mx4_buf, M, d)});
 }
 
 }  // namespace larosa
