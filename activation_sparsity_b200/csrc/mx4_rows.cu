@@ -24,9 +24,8 @@
 //     bits, v = (p0 + 2^-11 p1) 2^(e - 14): what p0 leaves has up to 12 bits,
 //     so |error| <= 2^-23 |v| for entries within 2^-27 of the block's largest
 //     (below, 2^-50 of the largest); a third piece for the last bit would take
-//     half as many MMAs again.  The
-//     pieces are neighbouring columns of the B operand: 4 tokens x 2 pieces
-//     fill its 8 columns;
+//     half as many MMAs again.  The pieces are neighbouring columns of the B
+//     operand: 4 tokens x 2 pieces fill its 8 columns;
 //   * a block's product is a fresh accumulator, scaled by the two powers of
 //     two (the token's and the column's) when it is added to the fp32 sum.
 //
